@@ -107,6 +107,15 @@ SIGNATURES = {
     "swa_attn_extend_ws_bytes": (SZ, [P, I32, I64, I32]),
     "swa_attn_extend": (I32, [P, I32, I32, P, I64, P, P, P, P, I64, I32, I32, P, P, P, F32, F32,
                               F32, P, P, SZ, P]),
+    "swa_tree_bytes": (SZ, [P, I64, I32]),
+    "swa_tree_plan": (I32, [P, I32, P, P, P, I64, I32, P, P, SZ, P]),
+    "swa_attn_tree_ws_bytes": (SZ, [P, I32, I32, I64, I32, I32]),
+    "swa_attn_tree": (I32, [P, I32, I32, P, I64, P, P, P, I64, I32, I32, P, P, P, P, F32, F32, F32,
+                            P, P, SZ, P]),
+    "swa_qk_norm_rope_store": (I32, [P, I32, P, I64, P, I64, P, I64, I64, P, P, P, F32, P, I64, I32,
+                                     I32, P, P, F32, F32, P, P]),
+    "swa_commit_tree": (I32, [P, I32, P, I64, P, P, P, I32, P, P]),
+    "swa_copy_kv": (I32, [P, P, P, I64, P]),
     "swa_last_attn_path": (I32, [P]),
     "swa_set_attn_path": (I32, [P, I32]),
     "swa_synth_tokens": (I32, [C.c_uint64, I32, I32, P, P, I64, I32, I32, I32, P, P]),
@@ -520,6 +529,79 @@ def swa_attn_extend(ctx, layer, req_to_token, req_idx, prefix_lens, seq_lens, qo
                                  max_new, max_seq_len, _ptr(plan), _ptr(q), _ptr(sinks), sm_scale,
                                  k_scale, v_scale, _ptr(out), _ptr(ws), ws.numel(),
                                  _stream(stream)), ctx.handle)
+
+
+# ------------------------------------------------------- speculative step ---
+TREE_MAX_NODES = 1024
+
+
+def swa_tree_bytes(ctx, n_tokens, max_new):
+    return lib().swa_tree_bytes(ctx.handle, n_tokens, max_new)
+
+
+def swa_tree_plan(ctx, parents, prefix_lens, qo_indptr, n_tokens, max_new, tree, positions=None,
+                  stream=None):
+    """Depths, positions and ancestor sets of the batch's drafted nodes."""
+    _check(lib().swa_tree_plan(ctx.handle, prefix_lens.numel(), _ptr(parents), _ptr(prefix_lens),
+                               _ptr(qo_indptr), n_tokens, max_new, _ptr(positions), _ptr(tree),
+                               tree.numel(), _stream(stream)), ctx.handle)
+
+
+def swa_attn_tree_ws_bytes(ctx, layer, bs, n_tokens, max_new, max_seq_len):
+    return lib().swa_attn_tree_ws_bytes(ctx.handle, layer, bs, n_tokens, max_new, max_seq_len)
+
+
+def swa_attn_tree(ctx, layer, req_to_token, req_idx, prefix_lens, qo_indptr, n_tokens, max_new,
+                  max_seq_len, plan, tree, q, sinks, sm_scale, out, ws, k_scale=1.0, v_scale=1.0,
+                  stream=None):
+    bs = prefix_lens.numel()
+    stride = req_to_token.shape[1] if req_to_token is not None else 0
+    _check(lib().swa_attn_tree(ctx.handle, layer, bs, _ptr(req_to_token), stride, _ptr(req_idx),
+                               _ptr(prefix_lens), _ptr(qo_indptr), n_tokens, max_new, max_seq_len,
+                               _ptr(plan), _ptr(tree), _ptr(q), _ptr(sinks), sm_scale, k_scale,
+                               v_scale, _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
+           ctx.handle)
+
+
+def _rows_ptr(t):
+    """[n, heads, D] rows that may be strided over tokens -> (pointer, elements between tokens)."""
+    if t is None:
+        return None, 0
+    assert t.is_cuda, "device buffer expected"
+    assert t.dim() == 3 and t.stride(2) == 1 and t.stride(1) == t.shape[2], \
+        "heads of a token must be contiguous"
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def swa_qk_norm_rope_store(ctx, layer, q, k, v, positions, full_loc, q_out, swa_loc=None,
+                           q_weight=None, k_weight=None, eps=1e-6, cos_sin=None, rot_dim=0,
+                           interleaved=False, k_scale=1.0, v_scale=1.0, stream=None):
+    """q, k, v: [n, heads, D], possibly slices of one fused projection; any of
+    q (with q_out) or k and v may be None."""
+    qp, qs = _rows_ptr(q)
+    kp, ks = _rows_ptr(k)
+    vp, vs = _rows_ptr(v)
+    n = (q if q is not None else k).shape[0]
+    _check(lib().swa_qk_norm_rope_store(
+        ctx.handle, layer, qp, qs, kp, ks, vp, vs, n, _ptr(positions), _ptr(q_weight),
+        _ptr(k_weight), eps, _ptr(cos_sin), cos_sin.shape[0] if cos_sin is not None else 0, rot_dim,
+        1 if interleaved else 0, _ptr(full_loc), _ptr(swa_loc), k_scale, v_scale, _ptr(q_out),
+        _stream(stream)), ctx.handle)
+
+
+def swa_commit_tree(ctx, req_to_token, req_idx, prefix_lens, accepted, n_accepted, stream=None):
+    """accepted: [bs, max_accept] int32 node indices, ascending; n_accepted: [bs] int32."""
+    _check(lib().swa_commit_tree(ctx.handle, prefix_lens.numel(), _ptr(req_to_token),
+                                 req_to_token.shape[1], _ptr(req_idx), _ptr(prefix_lens),
+                                 _ptr(accepted), accepted.shape[1], _ptr(n_accepted),
+                                 _stream(stream)), ctx.handle)
+
+
+def swa_copy_kv(ctx, src, dst, stream=None):
+    """K/V rows of all layers from full slots src to dst (-1 skips an entry)."""
+    assert src.numel() == dst.numel()
+    _check(lib().swa_copy_kv(ctx.handle, _ptr(src), _ptr(dst), src.numel(), _stream(stream)),
+           ctx.handle)
 
 
 def swa_last_attn_path(ctx):

@@ -18,12 +18,17 @@
 // writes the output (one split) or a partial (m, l, acc); the last CTA of a
 // (query, KV head) to finish - found with an atomic ticket - merges the
 // partials, folds in the sink and resets the ticket, so one launch does both.
+//
+// Tree attention (kTree): query i is a node of its request's draft tree, at
+// column prefix + node of req_to_token; it walks the cached columns of its
+// window and then the columns of nodes 0 .. node, skipping those that its
+// ancestor bit row does not name (warp-uniform: one query per CTA).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
-#include "swa_internal.h"
+#include "spec_internal.h"
 
 namespace swa {
 namespace {
@@ -56,6 +61,8 @@ struct SimtParams {
   int max_splits;
   int split_keys;             // keys per split, a power of two in [kMinSplit, kSplit]
   int32_t *err;
+  TreeView tree;              // tree attention only
+  int max_new;
 };
 
 template <typename T> struct Elem;
@@ -118,21 +125,59 @@ __device__ inline int64_t slot_of(const SimtParams &P, int b, int64_t j) {
   return page * P.ps + j % P.ps;
 }
 
-template <typename KT, typename QT, int DL>
+// Tree attention: the request, node and key columns [lo, hi) of query i; false
+// for rows that belong to no request or node.
+__device__ inline bool locate_node(const SimtParams &P, int i, int &b, int64_t &prefix, int64_t &lo,
+                                   int64_t &hi, const uint32_t *&mask) {
+  int64_t p;
+  locate_query(P, i, b, p);
+  const int64_t q0 = P.qo_indptr[b], node = i - q0;
+  prefix = P.pre[b];
+  if (node < 0 || i >= P.qo_indptr[b + 1] || node >= P.max_new || prefix < 0) return false;
+  hi = prefix + node + 1;
+  if (P.rt && hi > P.rt_stride) {
+    set_error(P.err, SWA_DEVERR_RANGE);
+    return false;
+  }
+  const int depth = P.tree.depth[i];
+  mask = P.tree.mask + (int64_t)i * P.tree.words;
+  lo = tree_first_col(key_lo(P.kind, P.window, prefix + depth), prefix, (int)node, depth, mask);
+  // More keys than the grid and the workspace were sized for.
+  const int64_t most = (int64_t)P.max_splits * P.split_keys;
+  if (hi - lo > most) {
+    set_error(P.err, SWA_DEVERR_RANGE);
+    return false;
+  }
+  return true;
+}
+
+template <typename KT, typename QT, int DL, bool kTree>
 __global__ void __launch_bounds__(kWarps * 32) k_attn_simt(SimtParams P) {
   constexpr int D = DL * 32;
   const int split = blockIdx.x, kvh = blockIdx.y, qi = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = P.G;
   int b;
-  int64_t p;
-  locate_query(P, qi, b, p);
-  const int64_t lo = key_lo(P.kind, P.window, p);
+  int64_t p, lo, prefix = 0;
+  const uint32_t *mask = nullptr;   // the node's ancestor bit row
+  if constexpr (kTree) {
+    if (!locate_node(P, qi, b, prefix, lo, p, mask)) return;
+    --p;
+  } else {
+    locate_query(P, qi, b, p);
+    lo = key_lo(P.kind, P.window, p);
+  }
   const int64_t n_keys = p - lo + 1;
   const int n_splits = (int)((n_keys + P.split_keys - 1) / P.split_keys);
   if (split >= n_splits) return;
   const int64_t k0 = lo + (int64_t)split * P.split_keys;
   const int64_t k1 = min(p + 1, k0 + P.split_keys);
+  // Whether key i of the split counts.
+  auto seen = [&](int i) {
+    if constexpr (!kTree) return true;
+    const int64_t node = k0 + i - prefix;
+    return node < 0 || ((mask[node >> 5] >> (node & 31)) & 1u) != 0u;
+  };
 
   __shared__ float qs[kGMax][D];
   __shared__ float sm_m[kWarps][kGMax], sm_l[kWarps][kGMax];
@@ -207,6 +252,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_simt(SimtParams P) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (i0 + u * kWarps >= nk) break;
+      if (!seen(i0 + u * kWarps)) continue;
 #pragma unroll
       for (int g = 0; g < kGMax; ++g) {
         if (g < G) {
@@ -313,14 +359,13 @@ struct WsLayout {
   int split_keys;
 };
 
-WsLayout ws_layout(const Ctx &c, int layer, int64_t nq, int max_seq_len) {
+WsLayout ws_layout(const Ctx &c, int layer, int64_t nq, int mk) {
   WsLayout w;
   const LayerInfo &L = c.layers[layer];
   const int G = c.cfg.num_q_heads / L.hkv;
   // Split size: the longest (kSplit) unless the launch would then fill less
   // than one wave of 2 CTAs per SM; small batches cut their keys finer so
   // more CTAs walk them in parallel (partials merged in the same launch).
-  const int mk = max_keys(c, layer, max_seq_len);
   const int64_t slots = 2LL * (c.num_sms > 0 ? c.num_sms : 148);
   w.split_keys = kSplit;
   while (w.split_keys > kMinSplit &&
@@ -333,12 +378,12 @@ WsLayout ws_layout(const Ctx &c, int layer, int64_t nq, int max_seq_len) {
   return w;
 }
 
-template <typename KT, typename QT>
+template <typename KT, typename QT, bool kTree>
 cudaError_t dispatch_dl(int D, dim3 grid, const SimtParams &P, cudaStream_t s) {
   switch (D) {
-    case 32: k_attn_simt<KT, QT, 1><<<grid, kWarps * 32, 0, s>>>(P); break;
-    case 64: k_attn_simt<KT, QT, 2><<<grid, kWarps * 32, 0, s>>>(P); break;
-    case 128: k_attn_simt<KT, QT, 4><<<grid, kWarps * 32, 0, s>>>(P); break;
+    case 32: k_attn_simt<KT, QT, 1, kTree><<<grid, kWarps * 32, 0, s>>>(P); break;
+    case 64: k_attn_simt<KT, QT, 2, kTree><<<grid, kWarps * 32, 0, s>>>(P); break;
+    case 128: k_attn_simt<KT, QT, 4, kTree><<<grid, kWarps * 32, 0, s>>>(P); break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();
@@ -347,14 +392,25 @@ cudaError_t dispatch_dl(int D, dim3 grid, const SimtParams &P, cudaStream_t s) {
 }  // namespace
 
 size_t simt_ws_bytes(const Ctx &c, int layer, int64_t nq, int max_seq_len) {
-  return ws_layout(c, layer, nq, max_seq_len).total;
+  return ws_layout(c, layer, nq, max_keys(c, layer, max_seq_len)).total;
 }
 
-cudaError_t launch_attn_simt(Ctx &c, const AttnArgs &a, cudaStream_t s) {
-  if (a.nq == 0) return cudaSuccess;
+int64_t tree_max_keys(const Ctx &c, int layer, int max_new, int max_seq_len) {
+  const LayerInfo &L = c.layers[layer];
+  int64_t mk = max_seq_len;
+  if (L.kind != SWA_LAYER_FULL && (int64_t)L.window + max_new < mk) mk = (int64_t)L.window + max_new;
+  return mk;
+}
+
+size_t simt_tree_ws_bytes(const Ctx &c, int layer, int64_t nq, int max_new, int max_seq_len) {
+  return ws_layout(c, layer, nq, (int)tree_max_keys(c, layer, max_new, max_seq_len)).total;
+}
+
+namespace {
+
+SimtParams simt_params(const Ctx &c, const AttnArgs &a, const WsLayout &w) {
   const LayerInfo &L = c.layers[a.layer];
-  WsLayout w = ws_layout(c, a.layer, a.nq, a.max_seq_len);
-  SimtParams P;
+  SimtParams P{};
   P.kind = L.kind;
   P.window = L.window;
   P.hkv = L.hkv;
@@ -383,11 +439,34 @@ cudaError_t launch_attn_simt(Ctx &c, const AttnArgs &a, cudaStream_t s) {
   P.max_splits = w.max_splits;
   P.split_keys = w.split_keys;
   P.err = c.err_word;
-  dim3 grid(w.max_splits, L.hkv, a.nq);
-  if (c.cfg.kv_dtype == SWA_DTYPE_F32) return dispatch_dl<float, float>(P.D, grid, P, s);
+  return P;
+}
+
+template <bool kTree>
+cudaError_t launch_simt(const Ctx &c, const SimtParams &P, const AttnArgs &a, cudaStream_t s) {
+  dim3 grid(P.max_splits, P.hkv, a.nq);
+  if (c.cfg.kv_dtype == SWA_DTYPE_F32) return dispatch_dl<float, float, kTree>(P.D, grid, P, s);
   if (c.cfg.kv_dtype == SWA_DTYPE_BF16)
-    return dispatch_dl<__nv_bfloat16, __nv_bfloat16>(P.D, grid, P, s);
-  return dispatch_dl<__nv_fp8_e4m3, __nv_bfloat16>(P.D, grid, P, s);
+    return dispatch_dl<__nv_bfloat16, __nv_bfloat16, kTree>(P.D, grid, P, s);
+  return dispatch_dl<__nv_fp8_e4m3, __nv_bfloat16, kTree>(P.D, grid, P, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_simt(Ctx &c, const AttnArgs &a, cudaStream_t s) {
+  if (a.nq == 0) return cudaSuccess;
+  const WsLayout w = ws_layout(c, a.layer, a.nq, max_keys(c, a.layer, a.max_seq_len));
+  return launch_simt<false>(c, simt_params(c, a, w), a, s);
+}
+
+cudaError_t launch_attn_tree_simt(Ctx &c, const AttnArgs &a, const TreeView &tree, cudaStream_t s) {
+  if (a.nq == 0) return cudaSuccess;
+  const WsLayout w =
+      ws_layout(c, a.layer, a.nq, (int)tree_max_keys(c, a.layer, a.max_new, a.max_seq_len));
+  SimtParams P = simt_params(c, a, w);
+  P.tree = tree;
+  P.max_new = a.max_new;
+  return launch_simt<true>(c, P, a, s);
 }
 
 }  // namespace swa

@@ -10,6 +10,7 @@
 #include <new>
 #include <string>
 
+#include "spec_internal.h"
 #include "swa_internal.h"
 
 struct swa_ctx : public swa::Ctx {
@@ -736,6 +737,179 @@ swa_status swa_attn_extend(swa_ctx *c, int32_t layer, int32_t bs, const int32_t 
     c->last_path = 0;
     CUDA_TRY(c, swa::launch_attn_simt(*c, a, s));
   }
+  return SWA_OK;
+}
+
+// --------------------------------------------------------- speculative step ---
+size_t swa_tree_bytes(const swa_ctx *c, int64_t n_tokens, int32_t max_new) {
+  if (!c || n_tokens < 0 || max_new < 1 || max_new > SWA_TREE_MAX_NODES) return 0;
+  const size_t row = (size_t)((max_new + 31) / 32) * sizeof(uint32_t);
+  return al256(swa::tree_depth_bytes(n_tokens) + (size_t)n_tokens * row + 1);
+}
+
+swa_status swa_tree_plan(swa_ctx *c, int32_t bs, const int32_t *parents,
+                         const int64_t *prefix_lens, const int64_t *qo_indptr, int64_t n_tokens,
+                         int32_t max_new, int64_t *positions, void *tree, size_t tree_bytes,
+                         swa_stream_t stream) {
+  SWA_NVTX("swa_tree_plan");
+  if (!c) return SWA_ERR_INVALID;
+  if (bs < 0 || bs > c->cfg.max_batch || n_tokens < 0)
+    return fail(c, SWA_ERR_INVALID, "bs out of range");
+  if (max_new < 1 || max_new > SWA_TREE_MAX_NODES)
+    return fail(c, SWA_ERR_INVALID, "max_new must be 1 .. SWA_TREE_MAX_NODES");
+  if (bs == 0 || n_tokens == 0) return SWA_OK;
+  if (!parents || !prefix_lens || !qo_indptr || !tree)
+    return fail(c, SWA_ERR_INVALID, "bad tree plan args");
+  if (tree_bytes < swa_tree_bytes(c, n_tokens, max_new))
+    return fail(c, SWA_ERR_INVALID, "tree buffer too small");
+  CUDA_TRY(c, swa::launch_tree_plan(*c, bs, parents, prefix_lens, qo_indptr, n_tokens, max_new,
+                                    positions, swa::tree_view(tree, n_tokens, max_new),
+                                    (cudaStream_t)stream));
+  return SWA_OK;
+}
+
+size_t swa_attn_tree_ws_bytes(const swa_ctx *c, int32_t layer, int32_t bs, int64_t n_tokens,
+                              int32_t max_new, int32_t max_seq_len) {
+  if (!c || layer < 0 || layer >= c->cfg.num_layers || bs < 0 || n_tokens < 0 || max_new < 1 ||
+      max_new > SWA_TREE_MAX_NODES || max_seq_len < 1)
+    return 0;
+  return swa::simt_tree_ws_bytes(*c, layer, n_tokens, max_new, max_seq_len);
+}
+
+swa_status swa_attn_tree(swa_ctx *c, int32_t layer, int32_t bs, const int32_t *rt,
+                         int64_t rt_stride, const int64_t *req_idx, const int64_t *prefix_lens,
+                         const int64_t *qo_indptr, int64_t n_tokens, int32_t max_new,
+                         int32_t max_seq_len, const void *plan, const void *tree, const void *q,
+                         const float *sinks, float sm_scale, float k_scale, float v_scale,
+                         void *out, void *ws, size_t ws_bytes, swa_stream_t stream) {
+  SWA_NVTX("swa_attn_tree");
+  if (!c) return SWA_ERR_INVALID;
+  if (layer < 0 || layer >= c->cfg.num_layers) return fail(c, SWA_ERR_INVALID, "layer out of range");
+  if (bs < 0 || bs > c->cfg.max_batch || n_tokens < 0)
+    return fail(c, SWA_ERR_INVALID, "bs out of range");
+  if (max_new < 1 || max_new > SWA_TREE_MAX_NODES)
+    return fail(c, SWA_ERR_INVALID, "max_new must be 1 .. SWA_TREE_MAX_NODES");
+  if (bs == 0 || n_tokens == 0) return SWA_OK;
+  const swa::LayerInfo &L = c->layers[layer];
+  if (!prefix_lens || !qo_indptr || !tree || !q || !out || max_seq_len < 1 ||
+      (L.in_full && (!rt || !req_idx)) || (!L.in_full && !plan))
+    return fail(c, SWA_ERR_INVALID, "bad attention args");
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15)
+    return fail(c, SWA_ERR_INVALID, "q and out must be 16-byte aligned");
+  if (!ws || ws_bytes < swa_attn_tree_ws_bytes(c, layer, bs, n_tokens, max_new, max_seq_len))
+    return fail(c, SWA_ERR_INVALID, "split workspace too small");
+  if (n_tokens > 65535)
+    return fail(c, SWA_ERR_INVALID, "n_tokens > 65535 on the generic path");
+  swa::AttnArgs a{};
+  a.layer = layer;
+  a.nq = (int)n_tokens;
+  a.bs = bs;
+  a.rt = rt;
+  a.rt_stride = rt_stride;
+  a.req_idx = req_idx;
+  a.pre = prefix_lens;
+  a.qo_indptr = qo_indptr;
+  a.max_seq_len = max_seq_len;
+  a.max_new = max_new;
+  a.plan = plan_view(c, plan, bs, max_new);
+  a.q = q;
+  a.sinks = sinks;
+  a.scale = sm_scale;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.out = out;
+  a.ws = ws;
+  a.ws_bytes = ws_bytes;
+  const swa::TreeView tv = swa::tree_view(tree, n_tokens, max_new);
+  c->last_path = 0;
+  CUDA_TRY(c, swa::launch_attn_tree_simt(*c, a, tv, (cudaStream_t)stream));
+  return SWA_OK;
+}
+
+swa_status swa_qk_norm_rope_store(swa_ctx *c, int32_t layer, const void *q, int64_t q_stride,
+                                  const void *k, int64_t k_stride, const void *v,
+                                  int64_t v_stride, int64_t n, const int64_t *positions,
+                                  const float *q_weight, const float *k_weight, float eps,
+                                  const float *cos_sin, int64_t max_pos, int32_t rot_dim,
+                                  int32_t interleaved, const int64_t *full_loc,
+                                  const int64_t *swa_loc, float k_scale, float v_scale,
+                                  void *q_out, swa_stream_t stream) {
+  SWA_NVTX("swa_qk_norm_rope_store");
+  if (!c) return SWA_ERR_INVALID;
+  if (layer < 0 || layer >= c->cfg.num_layers) return fail(c, SWA_ERR_INVALID, "layer out of range");
+  if (n < 0 || n > 0x7fffffff) return fail(c, SWA_ERR_INVALID, "token count out of range");
+  if (n == 0) return SWA_OK;
+  if (!q && !k) return fail(c, SWA_ERR_INVALID, "neither q nor k given");
+  if ((q != nullptr) != (q_out != nullptr))
+    return fail(c, SWA_ERR_INVALID, "q and q_out go together");
+  if ((k != nullptr) != (v != nullptr) || (k && !full_loc))
+    return fail(c, SWA_ERR_INVALID, "k, v and full_loc go together");
+  if (rot_dim < 0 || rot_dim > c->cfg.head_dim || rot_dim % 16 ||
+      (rot_dim > 0 && (!positions || !cos_sin || max_pos < 1)))
+    return fail(c, SWA_ERR_INVALID,
+                "rot_dim must be a multiple of 16 up to head_dim, with positions and a table");
+  if (!(eps >= 0)) return fail(c, SWA_ERR_INVALID, "eps must be >= 0");
+  if (k && c->cfg.kv_dtype == SWA_DTYPE_E4M3 && (!(k_scale > 0) || !(v_scale > 0)))
+    return fail(c, SWA_ERR_INVALID, "fp8 scales must be > 0");
+  // Head rows move as 16-byte words.
+  const int64_t esz = c->cfg.kv_dtype == SWA_DTYPE_F32 ? 4 : 2;
+  const int64_t d = c->cfg.head_dim, hkv = c->layers[layer].hkv;
+  auto bad = [&](const void *p, int64_t stride, int64_t heads) {
+    return p && ((reinterpret_cast<uintptr_t>(p) & 15) || (stride * esz) % 16 || stride < heads * d);
+  };
+  if (bad(q, q_stride, c->cfg.num_q_heads) || bad(k, k_stride, hkv) || bad(v, v_stride, hkv) ||
+      (reinterpret_cast<uintptr_t>(q_out) & 15))
+    return fail(c, SWA_ERR_INVALID,
+                "q, k, v and q_out need 16-byte aligned rows that do not overlap");
+  swa::QkNormArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.n = n;
+  a.positions = positions;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.max_pos = max_pos;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.full_loc = full_loc;
+  a.swa_loc = swa_loc;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.q_out = q_out;
+  CUDA_TRY(c, swa::launch_qk_norm_rope_store(*c, layer, a, (cudaStream_t)stream));
+  return SWA_OK;
+}
+
+swa_status swa_copy_kv(swa_ctx *c, const int64_t *src, const int64_t *dst, int64_t n,
+                       swa_stream_t stream) {
+  SWA_NVTX("swa_copy_kv");
+  if (!c) return SWA_ERR_INVALID;
+  if (n < 0 || n > 0x7fffffff || (n > 0 && (!src || !dst)))
+    return fail(c, SWA_ERR_INVALID, "bad copy args");
+  CUDA_TRY(c, swa::launch_copy_kv(*c, src, dst, n, (cudaStream_t)stream));
+  return SWA_OK;
+}
+
+swa_status swa_commit_tree(swa_ctx *c, int32_t bs, const int32_t *rt, int64_t rt_stride,
+                           const int64_t *req_idx, const int64_t *prefix_lens,
+                           const int32_t *accepted, int32_t max_accept, const int32_t *n_accepted,
+                           swa_stream_t stream) {
+  SWA_NVTX("swa_commit_tree");
+  if (!c) return SWA_ERR_INVALID;
+  if (bs < 0 || bs > c->cfg.max_batch) return fail(c, SWA_ERR_INVALID, "bs out of range");
+  if (max_accept < 0 || max_accept > SWA_TREE_MAX_NODES)
+    return fail(c, SWA_ERR_INVALID, "max_accept must be 0 .. SWA_TREE_MAX_NODES");
+  if (bs == 0 || max_accept == 0) return SWA_OK;
+  if (!rt || rt_stride < 1 || !req_idx || !prefix_lens || !accepted || !n_accepted)
+    return fail(c, SWA_ERR_INVALID, "bad commit args");
+  CUDA_TRY(c, swa::launch_commit_tree(*c, bs, rt, rt_stride, req_idx, prefix_lens, accepted,
+                                      max_accept, n_accepted, (cudaStream_t)stream));
   return SWA_OK;
 }
 

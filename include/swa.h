@@ -613,6 +613,116 @@ swa_status swa_attn_extend(swa_ctx *ctx, int32_t layer, int32_t bs,
                            float v_scale, void *out, void *ws, size_t ws_bytes,
                            swa_stream_t stream);
 
+/* ------------------------------------------------------ speculative step --
+ * A speculative decode step ([Pools 15], "how the sizes are set": a request
+ * takes swa_decode_alloc_sizes' slots per step for its draft tree): the drafted
+ * nodes of request b take columns prefix_lens[b] .. of req_to_token in node
+ * order (swa_alloc_extend), are stored there, attend as a tree, and the
+ * accepted path is moved to the front of them.  The source pages give the
+ * allocation; the four calls below are this library's own reading of the
+ * rest.
+ *
+ * Node i of a request (0-based) is a child of node parents[i] < i, or of the
+ * last cached token when parents[i] = -1; several nodes may hang there.  Its
+ * depth is its number of ancestors among the nodes, its position prefix +
+ * depth: a node's column and position differ once the tree branches.
+ *
+ * swa_tree_plan: depths, positions and ancestor sets of a batch's nodes, once
+ * per step for all layers.  Nodes of request b are entries qo_indptr[b] ..
+ * qo_indptr[b+1]-1 (device, bs+1 entries; a request may have none) of parents
+ * [n_tokens], positions [n_tokens] (nullable) and `tree` (swa_tree_bytes; any
+ * contents).  max_new (host, at most SWA_TREE_MAX_NODES) bounds a request's
+ * nodes; it and n_tokens are the same in every call on this tree.  A parent
+ * outside -1 .. i-1 sets SWA_DEVERR_RANGE and counts as -1; nodes past
+ * max_new or n_tokens set it and are left out. */
+enum { SWA_TREE_MAX_NODES = 1024 };
+size_t swa_tree_bytes(const swa_ctx *ctx, int64_t n_tokens, int32_t max_new);
+swa_status swa_tree_plan(swa_ctx *ctx, int32_t bs, const int32_t *parents,
+                         const int64_t *prefix_lens, const int64_t *qo_indptr,
+                         int64_t n_tokens, int32_t max_new, int64_t *positions,
+                         void *tree, size_t tree_bytes, swa_stream_t stream);
+
+/* swa_attn_tree: attention of every node over the request's cached keys and
+ * the node's own ancestors, itself included, of one layer:
+ *   keys of a node at position p: cached positions t < prefix with t >= lo(p),
+ *   and ancestors at positions >= lo(p),
+ * with lo(p) the first position its layer kind attends (0; max(0, p - window);
+ * floor(p/C)*C) and scale, sinks and output as above.  `tree` comes from
+ * swa_tree_plan, `plan` (SWA-pool layers) from swa_plan with the same
+ * prefix_lens, seq = prefix + nodes and the same max_new; max_seq_len bounds
+ * seq.  q, out: [n_tokens][Hq][D], 16-byte aligned, f32 for an F32 pool, bf16
+ * otherwise.  Rows of entries that belong to no request are left as they are.
+ * `ws` as for swa_attn_decode (zero before its first use, reusable; calls that
+ * may overlap on the GPU need their own). */
+size_t swa_attn_tree_ws_bytes(const swa_ctx *ctx, int32_t layer, int32_t bs,
+                              int64_t n_tokens, int32_t max_new,
+                              int32_t max_seq_len);
+swa_status swa_attn_tree(swa_ctx *ctx, int32_t layer, int32_t bs,
+                         const int32_t *req_to_token, int64_t rt_stride,
+                         const int64_t *req_idx, const int64_t *prefix_lens,
+                         const int64_t *qo_indptr, int64_t n_tokens,
+                         int32_t max_new, int32_t max_seq_len, const void *plan,
+                         const void *tree, const void *q, const float *sinks,
+                         float sm_scale, float k_scale, float v_scale, void *out,
+                         void *ws, size_t ws_bytes, swa_stream_t stream);
+
+/* swa_qk_norm_rope_store: what a layer does to its projections before
+ * attention, in one pass.  Every query and key head row x (D values) is
+ * normalised, y = x * weight / sqrt(mean(x^2) + eps) (weight NULL: y = x), and
+ * its first rot_dim values are rotated in pairs by the token's angles,
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * (a, b) = (y[i], y[i + rot_dim/2]), or (y[2i], y[2i+1]) when `interleaved`;
+ * cos_sin is [max_pos][rot_dim] floats, a position's rot_dim/2 cosines and then
+ * its sines (the caller's table, so any frequency scaling is in it).  Queries
+ * go to q_out [n][Hq][D], keys and values to `layer`'s pool as swa_store_kv
+ * stores them (E4M3: the float32 key is encoded without an intermediate
+ * rounding).  q, k, v: rows of token t at t * *_stride elements, heads
+ * contiguous (slices of one fused projection serve), f32 for an F32 pool, bf16
+ * otherwise; rows 16-byte aligned.  q_out may be q itself when q_stride = Hq *
+ * D.  q and q_out may be NULL (keys only), k and v may be NULL (queries only);
+ * rot_dim 0 rotates nothing (positions, cos_sin unused); otherwise it is a
+ * multiple of 16 up to D.  positions may be swa_tree_plan's.  A position
+ * outside the table sets SWA_DEVERR_RANGE and leaves the token's outputs and
+ * slots as they were; a slot outside the pool sets it and is not written. */
+swa_status swa_qk_norm_rope_store(swa_ctx *ctx, int32_t layer, const void *q,
+                                  int64_t q_stride, const void *k,
+                                  int64_t k_stride, const void *v,
+                                  int64_t v_stride, int64_t n,
+                                  const int64_t *positions,
+                                  const float *q_weight, const float *k_weight,
+                                  float eps, const float *cos_sin,
+                                  int64_t max_pos, int32_t rot_dim,
+                                  int32_t interleaved, const int64_t *full_loc,
+                                  const int64_t *swa_loc, float k_scale,
+                                  float v_scale, void *q_out,
+                                  swa_stream_t stream);
+
+/* swa_commit_tree: after verification, request b keeps nodes
+ * accepted[b*max_accept + j], j = 0 .. n_accepted[b]-1 (device; strictly
+ * ascending, so a path from the root): their K/V rows of every layer move from
+ * columns prefix + accepted[j] to prefix + j, in both pools.  The slots and
+ * req_to_token stay as they are; the request's length becomes prefix +
+ * n_accepted[b], and the caller frees the pages wholly past it (swa_free).  A
+ * list that is not strictly ascending, or reaches outside the row, sets
+ * SWA_DEVERR_RANGE: nothing moves from the offending entry on.  Rows that
+ * stay in place cost nothing. */
+swa_status swa_commit_tree(swa_ctx *ctx, int32_t bs, const int32_t *req_to_token,
+                           int64_t rt_stride, const int64_t *req_idx,
+                           const int64_t *prefix_lens, const int32_t *accepted,
+                           int32_t max_accept, const int32_t *n_accepted,
+                           swa_stream_t stream);
+
+/* swa_copy_kv: K/V rows of every layer from full slots src[i] to dst[i] (device,
+ * n entries), at their SWA slots on SWA-pool layers - a fork's open page, whose
+ * whole pages before it the two requests can share (the caller counts the
+ * sharers, as the radix tree does).  A source whose SWA slot was released is
+ * copied on full layers only.  -1 in either list skips the entry (padding).  No
+ * slot may be in both lists, or twice in dst.  A slot outside the pool, or a
+ * destination without the SWA slot its source has, sets the error word and is
+ * not copied. */
+swa_status swa_copy_kv(swa_ctx *ctx, const int64_t *src, const int64_t *dst,
+                       int64_t n, swa_stream_t stream);
+
 /* Which kernel family the last attention call on ctx launched
  * (0 = generic CUDA-core kernel, 1 = tensor-core decode fed by cp.async,
  * 2 = tcgen05 extend), for tests and profiling. */

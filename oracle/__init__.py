@@ -17,6 +17,8 @@ numpy / plain Python with float64 arithmetic for attention:
 * ``hitrule``    - the W-contiguous-non-tombstone prefix-hit rule.
 * ``kvstore``    - per-layer / envelope KV pools that store and gather rows.
 * ``radix``      - the SWA component of the radix prefix cache.
+* ``tree``       - draft trees (visible columns, attention, commit of accepted
+                   nodes), per-head q/k norm with rotation, row moves.
 * ``unified``    - the unified FULL/SWA pool allocated from both ends of one
                    page range, with its virtual-to-physical page tables.
 

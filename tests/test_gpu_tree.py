@@ -1,0 +1,384 @@
+"""Draft-tree plan and tree attention on the GPU against the oracle: every
+layer kind, head shape, type and layout, on the best kernel and on the generic
+one; trees of one node, chains, bushes and stars; requests without nodes or
+without cached tokens; windows shorter than the tree is deep; rows that belong
+to nobody; wide scores; graphs, streams and a shared workspace; refusals and
+device checks."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+from hybrid_sliding_window_gb300 import api  # noqa: E402
+from oracle import attention as OT  # noqa: E402
+from oracle import tree as TR  # noqa: E402
+from tests.harness import Pair  # noqa: E402
+from tests.spec_harness import TreeStep, assert_attention, dev, grow, random_parents  # noqa: E402
+
+MIMO = dict(Hq=64, D=128, dtype="bf16", layers=[(OT.SLIDING, 127, 8), (OT.FULL, 0, 4)])
+GPTOSS = dict(Hq=64, D=64, dtype="bf16", layers=[(OT.SLIDING, 127, 8), (OT.FULL, 0, 8)])
+LLAMA4 = dict(Hq=40, D=128, dtype="e4m3", layers=[(OT.CHUNKED, 192, 8), (OT.FULL, 0, 8)],
+              k_scale=0.41, v_scale=1.7)
+TINY = dict(Hq=4, D=64, dtype="f32", layers=[(OT.SLIDING, 15, 1), (OT.FULL, 0, 1)])
+
+
+def _pair(shape, ps, prompt, nodes, **kw):
+    kw = {**shape, **kw}
+    need = sum(-(-(p + n) // ps) * ps + ps for p, n in zip(prompt, nodes)) + 4 * ps
+    need = max(need, 1024 // ps * ps + 4 * ps)
+    layers = kw.pop("layers")
+    bs = len(prompt)
+    return Pair(layers, ps=ps, size_full=need, size_swa=need, seed=11, perm_free=True,
+                max_ctx=-(-(max(p + n for p, n in zip(prompt, nodes)) + 1) // 64) * 64,
+                max_reqs=bs, max_batch=max(64, bs), **kw)
+
+
+def _step(shape, ps, prompt, parents, path=-1, **kw):
+    P = _pair(shape, ps, prompt, [len(p) for p in parents], **kw)
+    api.swa_set_attn_path(P.ctx, path)
+    rows = list(range(1, len(prompt) + 1))
+    lens, _ = grow(P, rows, prompt)
+    S = TreeStep(P, rows, lens, parents)
+    P.check_state()
+    return P, S
+
+
+def _trees(seed, sizes):
+    rng = np.random.default_rng(seed)
+    return [random_parents(rng, n) for n in sizes]
+
+
+# ------------------------------------------------------------------- plan ---
+@pytest.mark.parametrize("sizes", [[1], [8, 0, 3], [32, 33, 31, 64], [200, 1, 77], [1024, 5]])
+def test_plan_depths_positions_and_ancestors(sizes):
+    P = _pair(TINY, 1, [5] * len(sizes), sizes)
+    rows = list(range(1, len(sizes) + 1))
+    lens, _ = grow(P, rows, [5 + b for b in range(len(sizes))])
+    trees = _trees(1, sizes)
+    trees[-1] = list(range(-1, sizes[-1] - 1))      # a chain
+    S = TreeStep(P, rows, lens, trees, store=False)
+    assert api.swa_device_check(P.ctx) == 0
+    n, words = S.n, (S.max_new + 31) // 32
+    raw = S.tree.cpu().numpy()
+    depth = raw[:4 * n].view(np.int32)
+    at = -(-4 * n // 256) * 256
+    mask = raw[at:at + 4 * n * words].view(np.uint32).reshape(n, words)
+    pos = S.positions.cpu().numpy()
+    for b, par in enumerate(trees):
+        for i, path in enumerate(TR.paths(par)):
+            r = S.indptr[b] + i
+            assert depth[r] == len(path) - 1 and pos[r] == S.pre[b] + len(path) - 1
+            bits = [j for j in range(32 * words) if mask[r, j >> 5] >> (j & 31) & 1]
+            assert bits == path
+
+
+def test_plan_flags_bad_parents_and_counts():
+    P = _pair(TINY, 1, [5, 9], [6, 6])
+    lens, _ = grow(P, [1, 2], [5, 9])
+    S = TreeStep(P, [1, 2], lens, [[-1, 0, 0, 2, 3, 3], [-1, 0, 1, 2, 3, 4]], store=False)
+    assert api.swa_device_check(P.ctx) == 0
+    good = S.positions.clone()
+    # a parent that is the node itself, or behind it, counts as the root
+    S.d["parents"].copy_(dev([-1, 0, 2, 2, 5, 3, -1, 0, -2, 2, 3, 4], torch.int32))
+    S.make_plans()
+    assert api.swa_device_check(P.ctx) == api.SWA_DEVERR_RANGE
+    assert S.positions.cpu().tolist() == [5, 6, 5, 6, 5, 7, 9, 10, 9, 10, 11, 12]
+    # more nodes than max_new: those are left out, the next call is clean
+    S.positions.fill_(-7)
+    api.swa_tree_plan(P.ctx, S.d["parents"], S.d["pre"], S.d["indptr"], S.n, 4, S.tree, S.positions)
+    assert api.swa_device_check(P.ctx) == api.SWA_DEVERR_RANGE
+    assert S.positions.cpu().tolist()[4:6] == [-7, -7]
+    # an indptr that ends behind the buffers
+    bad = dev([0, 6, 13])
+    S.positions.fill_(-7)
+    api.swa_tree_plan(P.ctx, S.d["parents"], S.d["pre"], bad, S.n, 16,
+                      torch.zeros(api.swa_tree_bytes(P.ctx, S.n, 16), dtype=torch.uint8, device="cuda"),
+                      S.positions)
+    assert api.swa_device_check(P.ctx) == api.SWA_DEVERR_RANGE
+    S.d["parents"].copy_(dev([-1, 0, 0, 2, 3, 3, -1, 0, 1, 2, 3, 4], torch.int32))
+    S.make_plans()
+    assert api.swa_device_check(P.ctx) == 0
+    assert torch.equal(S.positions, good)
+
+
+# -------------------------------------------------------------- attention ---
+CASES = [
+    pytest.param(MIMO, 64, "per_layer", id="mimo-ps64"),
+    pytest.param(MIMO, 16, "per_layer", id="mimo-ps16"),
+    pytest.param(MIMO, 1, "per_layer", id="mimo-ps1"),
+    pytest.param(GPTOSS, 16, "per_layer", id="gptoss-ps16"),
+    pytest.param(GPTOSS, 32, "envelope", id="gptoss-envelope-ps32"),
+    pytest.param(LLAMA4, 64, "envelope", id="llama4-envelope-ps64"),
+    pytest.param(LLAMA4, 16, "per_layer", id="llama4-ps16"),
+    pytest.param(TINY, 1, "per_layer", id="tiny-f32-ps1"),
+]
+
+
+@pytest.mark.parametrize("path", [-1, 0])
+@pytest.mark.parametrize("shape,ps,layout", CASES)
+def test_tree_attention(shape, ps, layout, path):
+    prompt = [700, 333, 0, 65, 1]
+    P, S = _step(shape, ps, prompt, _trees(3, [13, 1, 17, 33, 8]), path, layout=layout)
+    for l in range(len(P.layers)):
+        S.check(l, what=f"path {path}")
+        S.check(l, sinks=False, what=f"path {path}, no sinks")
+    assert api.swa_device_check(P.ctx) == 0
+
+
+@pytest.mark.parametrize("path", [-1, 0])
+@pytest.mark.parametrize("kind,window", [(OT.SLIDING, 3), (OT.SLIDING, 0), (OT.CHUNKED, 5),
+                                         (OT.CHUNKED, 1), (OT.SLIDING, 40)])
+def test_windows_shorter_than_the_tree(kind, window, path):
+    shape = dict(Hq=32, D=128, dtype="bf16", layers=[(kind, window, 4), (OT.FULL, 0, 4)])
+    rng = np.random.default_rng(5)
+    P, S = _step(shape, 16, [130, 47, 0, 12],
+                 [list(range(-1, 39)), random_parents(rng, 70, 0.02), list(range(-1, 19)), [-1] * 9], path)
+    for l in range(2):
+        S.check(l, what=f"window {window}")
+    assert api.swa_device_check(P.ctx) == 0
+
+
+@pytest.mark.parametrize("path", [-1, 0])
+@pytest.mark.parametrize("Hq,hkv,D", [(8, 8, 128), (24, 8, 128), (40, 8, 64), (16, 1, 128),
+                                      (12, 4, 64), (8, 4, 32)])
+def test_group_sizes(Hq, hkv, D, path):
+    shape = dict(Hq=Hq, D=D, dtype="bf16", layers=[(OT.SLIDING, 63, hkv), (OT.FULL, 0, hkv)])
+    P, S = _step(shape, 32, [200, 31, 150], _trees(7, [9, 140, 26]), path)
+    for l in range(2):
+        S.check(l, what=f"Hq {Hq} hkv {hkv}")
+    assert api.swa_device_check(P.ctx) == 0
+
+
+@pytest.mark.parametrize("shape", [MIMO, GPTOSS, LLAMA4], ids=["mimo", "gptoss", "llama4"])
+def test_many_requests_some_without_nodes(shape):
+    rng = np.random.default_rng(9)
+    n = 70
+    prompt = rng.integers(0, 300, n)
+    sizes = rng.integers(0, 21, n)
+    sizes[[0, 17, 33, 69]] = 0
+    P, S = _step(shape, 16, prompt.tolist(), _trees(10, sizes))
+    for l in range(2):
+        S.check(l, requests=[1, 2, 16, 18, 31, 32, 34, 50, 63, 64, 68], what="70 requests")
+    assert api.swa_device_check(P.ctx) == 0
+
+
+@pytest.mark.parametrize("shape", [MIMO, GPTOSS, LLAMA4], ids=["mimo", "gptoss", "llama4"])
+@pytest.mark.parametrize("nodes", [1, 8, 64, 300])
+def test_one_long_request(shape, nodes):
+    """Many key tiles of one request: its keys are split over the GPU and merged."""
+    P, S = _step(shape, 64, [4500], _trees(11, [nodes]))
+    for l in range(2):
+        g, q = S.attend(l)
+        some = sorted(set([0, nodes // 3, nodes - 1]))
+        slots = P.ort[1]
+        ref, mag = [], []
+        for i in some:
+            cols = TR.node_columns(P.layers[l][0], P.layers[l][1], 4500, S.parents[0], i)
+            sl = [int(slots[c]) for c in cols]
+            sl = sl if P.layers[l][0] == OT.FULL else [P.oa.mapping[s] for s in sl]
+            K, V = P.op.read(l, sl, P.k_scale, P.v_scale)
+            ref.append(OT.attend_heads(q[i], K, V, P.sinks[l], P.scale))
+            mag.append(OT.attend_heads(q[i], K, np.abs(V), P.sinks[l], P.scale))
+        assert_attention(g[some], np.stack(ref), np.stack(mag), P.dtype, f"{nodes} nodes layer {l}")
+    assert api.swa_device_check(P.ctx) == 0
+
+
+@pytest.mark.parametrize("path", [-1, 0])
+def test_rings(path):
+    P, S = _step(MIMO, 16, [200, 37, 130], _trees(12, [30, 17, 64]), path, ring_size=400)
+    for l in range(2):
+        S.check(l, what="ring")
+    assert api.swa_device_check(P.ctx) == 0
+
+
+@pytest.mark.parametrize("path", [-1, 0])
+@pytest.mark.parametrize("shape", [MIMO, LLAMA4], ids=["mimo", "llama4"])
+def test_wide_scores(shape, path):
+    """Scores that climb by hundreds along the keys (each key tile beats the one
+    before by more than any fixed reference holds) and sinks from -200 to 200.
+    The scores themselves then carry rounding: |score| up to ~1000, 128 products
+    in f32, so a weight may be off by 128 x 2^-24 x 1000 x 1.5 ~ 2^-6.5."""
+    P = _pair(shape, 64, [900, 420], [14, 9])
+    api.swa_set_attn_path(P.ctx, path)
+    P.q_gain = 16.0
+    P.k_gain = lambda t: 1 + (t % 512) / 16
+    for l in range(2):
+        P.set_sinks(l, np.linspace(-200, 200, P.Hq))
+    lens, _ = grow(P, [1, 2], [900, 420])
+    S = TreeStep(P, [1, 2], lens, _trees(13, [14, 9]))
+    for l in range(2):
+        g, q = S.attend(l)
+        at, ref, mag = S.oracle(l, q)
+        tol = 2 * (2.0 ** -8 + 2.0 ** -6.5) * mag + 2.0 ** -8 * np.abs(ref) + 1e-6
+        assert np.isfinite(g).all() and (np.abs(g[at] - ref) <= tol).all(), f"layer {l}"
+    assert api.swa_device_check(P.ctx) == 0
+
+
+def test_chain_equals_extend():
+    """A chain is the causal chunk that swa_attn_extend attends."""
+    P, S = _step(MIMO, 64, [700, 333], [list(range(-1, 39)), list(range(-1, 6))])
+    for l in range(2):
+        g, q = S.attend(l)
+        qd = P.to_dev(q)
+        out = torch.empty_like(qd)
+        ws = torch.zeros(api.swa_attn_extend_ws_bytes(P.ctx, l, S.n, S.max_seq), dtype=torch.uint8,
+                         device="cuda")
+        api.swa_attn_extend(P.ctx, l, P.rt, S.d["rows"], S.d["pre"], S.d["seq"], S.d["indptr"], S.n,
+                            S.max_new, S.max_seq, S.plan, qd, P.sinks_d[l], P.scale, out, ws)
+        at, _, mag = S.oracle(l, q)
+        # each within its own bound of the same sum
+        assert_attention(g, out.float().cpu().numpy(), 2 * mag, "bf16", f"layer {l}")
+
+
+@pytest.mark.parametrize("path", [-1, 0])
+@pytest.mark.parametrize("shape", [MIMO, LLAMA4, TINY], ids=["mimo", "llama4", "tiny"])
+def test_rows_of_nobody(shape, path):
+    """Query rows behind the last request's nodes stay as they were (positions
+    too), whatever they and their parents hold."""
+    ps = 1 if shape is TINY else 16
+    P = _pair(shape, ps, [90, 40], [9, 20])
+    api.swa_set_attn_path(P.ctx, path)
+    lens, _ = grow(P, [1, 2], [90, 40])
+    S = TreeStep(P, [1, 2], lens, _trees(14, [9, 20]), max_new=24)
+    for l in range(2):
+        want, q = S.attend(l)
+        n, pad = S.n, 5
+        qd = torch.cat([P.to_dev(q), torch.full((pad, P.Hq, P.D), float("nan"), dtype=P.to_dev(q).dtype,
+                                                device="cuda")])
+        out = torch.full_like(qd, 7.0)
+        tree = torch.full((api.swa_tree_bytes(P.ctx, n + pad, 24),), 0xA5, dtype=torch.uint8, device="cuda")
+        parents = torch.cat([S.d["parents"], dev([99] * pad, torch.int32)])
+        pos = torch.full((n + pad,), -3, dtype=torch.int64, device="cuda")
+        api.swa_tree_plan(P.ctx, parents, S.d["pre"], S.d["indptr"], n + pad, 24, tree, pos)
+        ws = torch.zeros(api.swa_attn_tree_ws_bytes(P.ctx, l, 2, n + pad, 24, S.max_seq),
+                         dtype=torch.uint8, device="cuda")
+        api.swa_attn_tree(P.ctx, l, P.rt, S.d["rows"], S.d["pre"], S.d["indptr"], n + pad, 24, S.max_seq,
+                          S.plan, tree, qd, P.sinks_d[l], P.scale, out, ws, P.k_scale, P.v_scale)
+        assert (out[n:] == 7).all() and (pos[n:] == -3).all()
+        np.testing.assert_array_equal(out[:n].float().cpu().numpy(), want)
+    assert api.swa_device_check(P.ctx) == 0
+
+
+def test_repeats_streams_and_graphs():
+    """One workspace for layers of other shapes, repeated calls, another stream
+    and replays of a captured step: bit for bit the same."""
+    P, S = _step(MIMO, 64, [2500, 333, 0, 65], _trees(15, [13, 1, 17, 33]))
+    n_ws = max(S.workspace(l).numel() for l in range(2))
+    ws = torch.zeros(n_ws, dtype=torch.uint8, device="cuda")
+    qs = [P.to_dev(S.queries(l)) for l in range(2)]
+    want = [torch.empty_like(q) for q in qs]
+    for l in range(2):
+        S.run(l, qs[l], want[l], S.workspace(l))
+    torch.cuda.synchronize()
+    outs = [torch.empty_like(q) for q in qs]
+    for _ in range(3):
+        for l in (1, 0):
+            S.run(l, qs[l], outs[l], ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    side = torch.cuda.Stream()
+    for o in outs:
+        o.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    S.make_plans(stream=side)
+    for l in range(2):
+        S.run(l, qs[l], outs[l], ws, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        S.make_plans()
+        for l in range(2):
+            S.run(l, qs[l], outs[l], ws)
+    for _ in range(2):
+        for o in outs:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    # the replay reads the tree and lengths that are there then
+    S.d["parents"].copy_(dev([-1] * S.n, torch.int32))
+    g.replay()
+    torch.cuda.synchronize()
+    S.parents = [[-1] * k for k in S.nodes]
+    for l in range(2):
+        q = S.queries(l)
+        at, ref, mag = S.oracle(l, q)
+        assert_attention(outs[l].float().cpu().numpy()[at], ref, mag, "bf16", "stars")
+    assert api.swa_device_check(P.ctx) == 0
+
+
+# ---------------------------------------------------------------- refusals ---
+def test_refusals_leave_the_context_usable():
+    P, S = _step(MIMO, 64, [100, 30], _trees(16, [5, 9]))
+    q = P.to_dev(S.queries(1))
+    out = torch.empty_like(q)
+    ws = S.workspace(1)
+    L, h = api.lib(), P.ctx.handle
+
+    def plan(**kw):
+        a = dict(bs=2, parents=S.d["parents"].data_ptr(), pre=S.d["pre"].data_ptr(),
+                 indptr=S.d["indptr"].data_ptr(), n=S.n, max_new=9, pos=None, tree=S.tree.data_ptr(),
+                 nb=S.tree.numel())
+        a.update(kw)
+        return L.swa_tree_plan(h, *a.values(), None)
+
+    def attn(**kw):
+        a = dict(layer=1, bs=2, rt=P.rt.data_ptr(), stride=P.rt.shape[1], rows=S.d["rows"].data_ptr(),
+                 pre=S.d["pre"].data_ptr(), indptr=S.d["indptr"].data_ptr(), n=S.n, max_new=9,
+                 msl=S.max_seq, plan=S.plan.data_ptr(), tree=S.tree.data_ptr(), q=q.data_ptr(),
+                 sinks=None, scale=0.1, ks=1.0, vs=1.0, out=out.data_ptr(), ws=ws.data_ptr(),
+                 nb=ws.numel())
+        a.update(kw)
+        return L.swa_attn_tree(h, *a.values(), None)
+
+    bad = api.SWA_ERR_INVALID
+    for kw in (dict(bs=-1), dict(bs=65), dict(n=-1), dict(max_new=0), dict(max_new=1025),
+               dict(parents=None), dict(pre=None), dict(indptr=None), dict(tree=None), dict(nb=8)):
+        assert plan(**kw) == bad, kw
+    for kw in (dict(layer=2), dict(layer=-1), dict(bs=-1), dict(bs=65), dict(n=-1), dict(max_new=0),
+               dict(max_new=1025), dict(msl=0), dict(rt=None), dict(rows=None), dict(pre=None),
+               dict(indptr=None), dict(tree=None), dict(q=None), dict(out=None), dict(ws=None),
+               dict(nb=16), dict(q=q.data_ptr() + 2), dict(out=out.data_ptr() + 8),
+               dict(layer=0, plan=None)):
+        assert attn(**kw) == bad, kw
+    assert api.swa_tree_bytes(P.ctx, 4, 1025) == 0 and api.swa_tree_bytes(P.ctx, -1, 4) == 0
+    assert api.swa_attn_tree_ws_bytes(P.ctx, 5, 2, 4, 4, 100) == 0
+    assert plan(bs=0) == 0 and plan(n=0) == 0 and attn(bs=0) == 0 and attn(n=0) == 0
+    assert plan() == 0 and attn() == 0
+    torch.cuda.synchronize()
+    assert api.swa_device_check(P.ctx) == 0
+    S.check(1, what="after refusals")
+
+
+def test_device_checks():
+    """Columns past the req_to_token row, and an evicted key in the window."""
+    P, S = _step(MIMO, 64, [700, 30], _trees(17, [5, 9]))
+    q = P.to_dev(S.queries(1))
+    out = torch.empty_like(q)
+    ws = S.workspace(1)
+    S.run(1, q, out, ws)
+    assert api.swa_device_check(P.ctx) == 0
+    # a prefix that puts the nodes past the row
+    good = S.d["pre"].clone()
+    S.d["pre"][1] = P.rt.shape[1] - 3
+    S.run(1, q, out, ws)
+    assert api.swa_device_check(P.ctx) & api.SWA_DEVERR_RANGE
+    S.d["pre"].copy_(good)
+    S.run(1, q, out, ws)
+    assert api.swa_device_check(P.ctx) == 0
+    # the SWA slot of a page inside the window released behind the plan's back
+    slot = int(P.ort[1, 690])
+    page = slot // 64 * 64
+    keep = P.ctx.mapping()[page:page + 64].clone()
+    P.ctx.mapping()[page:page + 64] = 0
+    S.make_plans()
+    assert api.swa_device_check(P.ctx) & api.SWA_DEVERR_WINDOW_EVICTED
+    P.ctx.mapping()[page:page + 64] = keep
+    S.make_plans()
+    for l in range(2):
+        S.check(l, what="after device checks")
+    assert api.swa_device_check(P.ctx) == 0
