@@ -1,0 +1,919 @@
+// Draft-tree attention on the 5th-generation tensor cores (tcgen05 + TMEM + TMA):
+// bf16 KV with D = 64 or 128, any GQA group, page size 16..64.
+//
+// Method: node i of a request reads the cached columns of its window and its
+// ancestors' columns behind the prefix (include/swa.h, swa_attn_tree).  With T
+// nodes and G query heads per KV head, T x G query rows share every K and V
+// row, 4 D T G flops on 4 D bytes (bf16): up to about 256 rows the kernel is
+// bound by reading the cache once, beyond that by the tensor cores and the
+// softmax between them.
+//
+// Work: an item is a block of up to 2 * floor(128 / G) nodes of one request for
+// one KV head; its keys are cut into tiles of 128 columns.  The tiles of all
+// items of one head form one line, and the CTAs of that head - groups =
+// #SMs / Hkv of them - take equal stretches of it, whatever the requests'
+// lengths are, so one long request fills the GPU and a ragged batch has no
+// tail.  CTAs of the same stretch and different heads are neighbours: a token's
+// head rows lie next to each other and are read at about the same time.  A
+// CTA's piece of an item is a segment.  Segments that hold an item's whole key
+// range write its output; the others write (max, sum, unnormalised output)
+// partials - at most two per CTA - which a second, dependent launch merges in
+// group order, so results do not depend on timing and the workspace needs no
+// initial contents.  Layers whose items have few keys (short windows) are dealt
+// out in whole items and need no second launch.
+//
+// A CTA (one per SM) has warp-specialised roles that meet on mbarriers, with
+// phases following running counts so that nothing drains between segments:
+//   * warp 9, the producer, finds the CTA's segments (warp-wide prefix sums over
+//     the requests), hands them to the other roles through a two-slot ring,
+//     looks page rows up 32 page slots at a time and streams K and V tiles by
+//     TMA through one ring, in the order in which the MMAs use them;
+//   * warp 10 loads each segment's Q tiles once the previous segment's last
+//     QK^T has read them;
+//   * warp 8 (one lane) issues S = Q K^T and O += P V with P in TMEM over S;
+//   * warps 0-3 and 4-7 are two softmax groups.  Rows of an item that fill two
+//     Q tiles: one tile each, both read the same key tiles.  Rows that fit one
+//     Q tile: the groups take alternate key tiles with an accumulator each, so
+//     that one group's softmax overlaps the other's products, and the two
+//     accumulators are joined in TMEM's own lanes at the segment's end (warps i
+//     and i + 4 can read the same lanes).
+// Key columns that some row may not read (window edge, non-ancestors) get -inf
+// scores from a 64-bit mask per row and 64-column chunk; chunks that no row of
+// a warp reads are skipped.
+// Every mbarrier wait has a poll limit; on expiry the kernel sets
+// SWA_DEVERR_TIMEOUT, every role leaves its loop, loads and products in flight
+// are waited for, and the TMEM is released.
+#include <algorithm>
+
+#include <math.h>
+
+#include <type_traits>
+
+#include "spec_internal.h"
+#include "tc_ptx.cuh"
+
+namespace swa {
+namespace {
+
+using namespace tc;
+
+constexpr int kTileRows = 128;               // rows of a Q tile (M)
+constexpr int kKeys = 128;                   // keys of a K/V tile
+constexpr int kBlock = kTileRows * 64 * 2;   // one 64-column block of a tile
+constexpr int kTreeThreads = 352;            // 8 softmax warps, MMA, producer, Q loader
+constexpr float kRescaleGap = 8.f;           // log2 units: rescale O when the max grows more
+constexpr float kSumCap = 32768.f;           // a chunk's weight sum that forces a maximum pass
+constexpr int kMergeThreads = 128;
+constexpr int kMergeRows = 16;               // rows of one merge CTA
+
+template <int D>
+struct TreeGeo {
+  static constexpr int kTileBytes = kKeys * D * 2;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kOffRing = 2 * kTileBytes;             // after the Q tiles
+  static constexpr int kOffStat = kOffRing + kStages * kTileBytes;
+  static constexpr int kOffBars = kOffStat + 2 * kTileRows * 8;
+  static constexpr int kOffCtl = kOffBars + 31 * 8 + 8;       // Control
+};
+
+struct TreeParams {
+  int kind, window, hkv, G, T, ps, ps_shift;   // T: nodes of a Q tile
+  int64_t page_stride, pool_rows;
+  const int32_t *rt;
+  int64_t rt_stride;
+  const int64_t *req_idx, *pre, *qo_indptr;
+  int bs, groups, max_new;
+  int whole;                 // 1: CTAs take whole items, nothing is merged
+  int64_t n_tokens;
+  PlanView plan;
+  TreeView tree;
+  const float *sinks;
+  float scale_log2;
+  __nv_bfloat16 *out;
+  float *partials;           // [CTA][2][rows x D, then rows x 2]
+  int64_t part_stride;       // floats of one partial
+  struct MergeDesc *desc;    // [CTA]
+  int32_t *err;
+};
+
+// A CTA's last segment when it starts an item that goes on in the next groups.
+struct MergeDesc {
+  int32_t parts;     // contributing CTAs (0: nothing to merge)
+  int32_t n_tok;     // nodes of the item
+  int64_t q0;        // first query row
+};
+
+struct Segment {
+  int b, n0, n_tok, n_tiles;   // request (-1: end), first node, nodes, key tiles
+  int two;                     // two Q tiles (else one, key tiles alternate)
+  int part;                    // -1: whole item; else the partial's slot
+  int64_t q0, col0, prefix;    // first query row, first key column, cached columns
+};
+
+// Shared words of the roles.  (Everything lives in the dynamic array, whose
+// start is 1024-byte aligned: the tiles leave no room for an alignment gap.)
+struct Control {
+  Segment seg[2];
+  int32_t rows[2][32];       // page rows of 32 page slots, double-buffered
+  uint32_t tmem;
+  int abort;
+};
+
+enum { B_IFULL = 0, B_IEMPTY = 2, B_FULLQ = 4, B_QFREE = 5, B_SDONE = 6, B_PREADY = 8,
+       B_ODONE = 10, B_STAT = 12, B_EPI = 13, B_DRAIN = 14, B_FULL = 15, B_EMPTY = 23,
+       B_COUNT = 31 };
+
+// Position in the ring of key tile i's K or V, of the n tiles of a segment: K0
+// K1 V0 K2 V1 ... - the order in which the products release them.
+__device__ __forceinline__ int seq_k(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int seq_v(int i, int n) { return min(2 * i + 2, 2 * n - 1); }
+
+// One request's nodes and keys as the schedule sees them.
+struct Request {
+  int64_t q0, prefix, col0, tiles;   // tiles: of all its blocks (items with `whole`)
+  int n, blocks;
+};
+__device__ __forceinline__ int64_t block_tiles(const TreeParams &P, const Request &r, int blk) {
+  if (P.whole) return 1;
+  const int last = min((blk + 1) * 2 * P.T, r.n);   // nodes up to the block's end
+  return ((r.prefix + last - 1 - r.col0) >> 7) + 1;
+}
+__device__ __forceinline__ Request request(const TreeParams &P, int b) {
+  Request r;
+  r.q0 = r.prefix = r.col0 = r.tiles = 0;
+  r.n = r.blocks = 0;
+  if (b >= P.bs) return r;
+  r.q0 = P.qo_indptr[b];
+  int64_t n = P.qo_indptr[b + 1] - r.q0;
+  r.prefix = P.pre[b];
+  if (n <= 0) return r;
+  const int64_t room = P.kind == SWA_LAYER_FULL ? P.rt_stride - r.prefix : n;
+  if (r.q0 < 0 || r.q0 + n > P.n_tokens || n > P.max_new || r.prefix < 0 || n > room) {
+    set_error(P.err, SWA_DEVERR_RANGE);
+    if (r.q0 < 0 || r.q0 >= P.n_tokens || r.prefix < 0 || room <= 0) return r;
+    n = min(min(n, P.n_tokens - r.q0), min((int64_t)P.max_new, room));
+  }
+  r.n = (int)n;
+  r.blocks = (r.n + 2 * P.T - 1) / (2 * P.T);
+  r.col0 = first_position(P.kind, P.window, r.prefix) >> P.ps_shift << P.ps_shift;
+  for (int i = 0; i < r.blocks; ++i) r.tiles += block_tiles(P, r, i);
+  return r;
+}
+
+// First row (in the layer's K/V view) of the page holding column `col`; rec is
+// its req_to_token entry (full layers) or its page in the request's plan, -1
+// when the plan has none.  An offending page reads as page 0.
+__device__ __forceinline__ int32_t page_rec(bool full, int ps_shift, const int32_t *rt_row,
+                                            const int32_t *hdr, const int32_t *pages, int64_t col) {
+  if (full) return rt_row[col];
+  const int64_t k = (col >> ps_shift) - hdr[2];
+  return (col >= hdr[0] && k >= 0 && k < hdr[3]) ? pages[k] : -1;
+}
+__device__ __forceinline__ int32_t page_row(const TreeParams &P, bool full, int32_t rec) {
+  int64_t page = full ? (rec >= 0 ? rec >> P.ps_shift : -1) : rec;
+  if (!full && page == 0) set_error(P.err, SWA_DEVERR_WINDOW_EVICTED);
+  if (page < 0 || page >= P.pool_rows >> P.ps_shift) {
+    set_error(P.err, SWA_DEVERR_RANGE);
+    page = 0;
+  }
+  return (int32_t)(page * P.page_stride);
+}
+
+// Bits [x, y) of a 64-bit mask, clipped to it.
+__device__ __forceinline__ uint64_t bit_range(int64_t x, int64_t y) {
+  x = max(x, (int64_t)0);
+  y = min(y, (int64_t)64);
+  if (x >= y) return 0ull;
+  return (~0ull >> (64 - (int)(y - x))) << (int)x;
+}
+// Bits o .. o + 63 of an ancestor row (o may be negative; zeros outside).
+__device__ __forceinline__ uint64_t row_bits(const uint32_t *row, int words, int64_t o) {
+  const int64_t w = o >> 5;
+  const int s = (int)(o & 31);
+  uint32_t x[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) x[i] = (w + i >= 0 && w + i < words) ? row[w + i] : 0u;
+  return (uint64_t)__funnelshift_r(x[0], x[1], s) | (uint64_t)__funnelshift_r(x[1], x[2], s) << 32;
+}
+
+template <int kD>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    k_tree_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+              const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TreeParams P) {
+  using Gm = TreeGeo<kD>;
+  constexpr int kTileBytes = Gm::kTileBytes, kStages = Gm::kStages;
+  static_assert(kStages <= 8, "barrier slots");
+  extern __shared__ __align__(1024) char smem[];
+  const uint32_t sb = smem_u32(smem);
+  float2 *s_stat = reinterpret_cast<float2 *>(smem + Gm::kOffStat);   // [group][row] max, sum
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Gm::kOffBars);
+  Control *ctl = reinterpret_cast<Control *>(smem + Gm::kOffCtl);
+  volatile int &s_abort = ctl->abort;
+  Segment *s_seg = ctl->seg;
+  auto &s_rows = ctl->rows;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int kvh = blockIdx.x % P.hkv, group_id = blockIdx.x / P.hkv;
+  const int G = P.G, T = P.T, TG = T * G;
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  auto wait_all = [&](uint32_t b, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(b, parity, &s_abort));
+  };
+
+  if (sb & 1023) {   // the operand layouts need it
+    if (tid == 0) set_error(P.err, SWA_DEVERR_RANGE);
+    return;
+  }
+  if (tid == 0) s_abort = 0;
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
+                     smem_u32(&ctl->tmem)),
+                 "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_IFULL + i), 1);
+      mbar_init(bar(B_IEMPTY + i), 10);   // 8 softmax warps, the MMA lane, the Q loader
+      mbar_init(bar(B_SDONE + i), 1);
+      mbar_init(bar(B_PREADY + i), kTileRows);
+      mbar_init(bar(B_ODONE + i), 1);
+    }
+    mbar_init(bar(B_FULLQ), 1);
+    mbar_init(bar(B_QFREE), 1);
+    mbar_init(bar(B_STAT), 2 * kTileRows);
+    mbar_init(bar(B_EPI), 2 * kTileRows);
+    mbar_init(bar(B_DRAIN), 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(B_FULL + i), 1);
+      mbar_init(bar(B_EMPTY + i), 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  constexpr uint32_t kIdS = idesc_f16(128, 128, false);
+  constexpr uint32_t kIdO = idesc_f16(128, kD, true);
+
+  // Loads issued, for the abort path: ring slots filled (producer), Q fills.
+  int ring_issued = 0, q_issued = 0;
+
+  if (warp == 9) {
+    // ===================== producer: segments, K/V tiles =====================
+    const bool full_layer = P.kind == SWA_LAYER_FULL;
+    const int ppt = kKeys >> P.ps_shift;     // pages per key tile
+    int n_pub = 0;
+    bool ok = true;
+    MergeDesc mine{0, 0, 0};
+    auto publish = [&](const Segment &sg) {
+      const int slot = n_pub & 1;
+      if (n_pub >= 2 && !wait_all(bar(B_IEMPTY + slot), ((n_pub >> 1) - 1) & 1)) return false;
+      if (lane == 0) {
+        s_seg[slot] = sg;
+        mbar_arrive(bar(B_IFULL + slot));
+      }
+      __syncwarp();
+      ++n_pub;
+      return true;
+    };
+    auto stream = [&](const Segment &sg, int64_t hi) {   // hi: the item's last column
+      const int32_t *rt_row = full_layer ? P.rt + P.req_idx[sg.b] * P.rt_stride : nullptr;
+      const int32_t *hdr = full_layer ? nullptr : P.plan.hdr + sg.b * 4;
+      const int32_t *pages = full_layer ? nullptr : P.plan.pages + (int64_t)sg.b * P.plan.max_pages;
+      const int64_t pg0 = sg.col0 >> P.ps_shift;
+      // A windowed request's first page may start before its first planned
+      // column: look it up by a column that is in the plan.
+      const int64_t lo = full_layer ? 0 : first_position(P.kind, P.window, sg.prefix);
+      const int n_pg = (int)((hi >> P.ps_shift) - pg0 + 1);
+      const int n_slots = sg.n_tiles * ppt;
+      // Page slots behind the last column load its page again: finite values,
+      // zero weight.
+      auto rec_of = [&](int k) {
+        const int i = min(32 * k + lane, n_pg - 1);
+        const int64_t col = max((pg0 + i) << P.ps_shift, lo);
+        return page_rec(full_layer, P.ps_shift, rt_row, hdr, pages, col);
+      };
+      s_rows[0][lane] = page_row(P, full_layer, rec_of(0));
+      int32_t rec_next = n_slots > 32 ? rec_of(1) : 0;
+      __syncwarp();
+      int cur = 0;                           // batch of 32 slots held in s_rows[cur & 1]
+      // Tiles in ring order: K0, then per tile the next K and this V.
+      for (int j = 0; j < 2 * sg.n_tiles && ok; ++j) {
+        const bool is_v = j == 2 * sg.n_tiles - 1 || (j > 0 && (j & 1) == 0);
+        const int t = is_v ? (j == 2 * sg.n_tiles - 1 ? sg.n_tiles - 1 : j / 2 - 1) : (j + 1) / 2;
+        const int i0 = t * ppt;
+        // K runs one tile ahead of V, so a batch's table stays until its last
+        // V is issued: two tables, the next one filled when K enters it.
+        if (!is_v && (i0 >> 5) > cur) {
+          cur = i0 >> 5;
+          s_rows[cur & 1][lane] = page_row(P, full_layer, rec_next);
+          rec_next = 32 * (cur + 1) < n_slots ? rec_of(cur + 1) : 0;
+          __syncwarp();
+        }
+        int good = 1;
+        if (lane == 0) {
+          const int s = ring_issued % kStages, f = ring_issued / kStages;
+          if (f >= 1) good = mbar_wait(bar(B_EMPTY + s), (f - 1) & 1, &s_abort);
+          if (good) {
+            const int32_t *rows = &s_rows[(i0 >> 5) & 1][i0 & 31];
+            const uint32_t dst = sb + Gm::kOffRing + s * kTileBytes, full = bar(B_FULL + s);
+            mbar_expect_tx(full, (uint32_t)kTileBytes);
+            for (int i = 0; i < ppt; ++i)
+              for (int h = 0; h < kD / 64; ++h)
+                tma_load_3d(dst + h * kBlock + (i << P.ps_shift) * 128, is_v ? &tmV : &tmK, h * 64,
+                            kvh, rows[i], full);
+            ++ring_issued;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+        __syncwarp();
+      }
+    };
+
+    // The head's line of tiles (or items), and this CTA's stretch of it.
+    int64_t total = 0;
+    for (int b0 = 0; b0 < P.bs; b0 += 32) total += request(P, b0 + lane).tiles;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const int64_t share = (total + P.groups - 1) / P.groups;
+    const int64_t w0 = group_id * share, w1 = min(total, w0 + share);
+    int64_t at = 0;                          // line position of the batch's first request
+    for (int b0 = 0; ok && b0 < P.bs && at < w1; b0 += 32) {
+      const Request r = request(P, b0 + lane);
+      int64_t incl = r.tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const int64_t s0 = at + incl - r.tiles;
+      unsigned hit = __ballot_sync(0xffffffffu, r.tiles > 0 && s0 < w1 && s0 + r.tiles > w0);
+      while (ok && hit) {
+        const int l = __ffs(hit) - 1;
+        hit &= hit - 1;
+        Request q;
+        q.q0 = __shfl_sync(0xffffffffu, r.q0, l);
+        q.prefix = __shfl_sync(0xffffffffu, r.prefix, l);
+        q.col0 = __shfl_sync(0xffffffffu, r.col0, l);
+        q.n = __shfl_sync(0xffffffffu, r.n, l);
+        q.blocks = __shfl_sync(0xffffffffu, r.blocks, l);
+        int64_t s = __shfl_sync(0xffffffffu, s0, l);
+        for (int blk = 0; ok && blk < q.blocks && s < w1; ++blk) {
+          const int64_t len = block_tiles(P, q, blk), e = s + len;
+          if (e > w0) {
+            const int64_t from = max(s, w0), to = min(e, w1);
+            Segment sg;
+            sg.b = b0 + l;
+            sg.n0 = blk * 2 * T;
+            sg.n_tok = min(2 * T, q.n - sg.n0);
+            sg.two = sg.n_tok > T;
+            sg.q0 = q.q0 + sg.n0;
+            sg.prefix = q.prefix;
+            sg.col0 = q.col0;
+            const int64_t hi = q.prefix + sg.n0 + sg.n_tok - 1;
+            sg.part = -1;
+            if (P.whole) {
+              sg.n_tiles = (int)(((hi - q.col0) >> 7) + 1);
+            } else {
+              sg.n_tiles = (int)(to - from);
+              sg.col0 += (from - s) * kKeys;
+              if (from == s && to < e) {
+                sg.part = 1;
+                mine.parts = (int)((e - 1) / share) - group_id + 1;
+                mine.n_tok = sg.n_tok;
+                mine.q0 = sg.q0;
+              } else if (from > s) {
+                sg.part = 0;
+              }
+            }
+            ok = publish(sg);
+            if (ok) stream(sg, hi);
+          }
+          s = e;
+        }
+      }
+      at += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (!P.whole && lane == 0) P.desc[blockIdx.x] = mine;
+    if (ok) {
+      Segment end{};
+      end.b = -1;
+      publish(end);
+    }
+  } else if (warp == 10) {
+    // ===================== Q tiles =====================
+    for (int nd = 0;; ++nd) {
+      const int slot = nd & 1;
+      if (!wait_all(bar(B_IFULL + slot), (nd >> 1) & 1)) break;
+      const Segment sg = s_seg[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
+      if (sg.b < 0) break;
+      if (nd >= 1 && !wait_all(bar(B_QFREE), (nd - 1) & 1)) break;
+      if (lane == 0) {
+        const int tiles = sg.two ? 2 : 1;
+        mbar_expect_tx(bar(B_FULLQ), (uint32_t)(tiles * TG * 128 * (kD / 64)));
+        for (int i = 0; i < tiles; ++i)
+          for (int h = 0; h < kD / 64; ++h)
+            tma_load_3d(sb + i * kTileBytes + h * kBlock, &tmQ, h * 64, kvh * G,
+                        (int)(sg.q0 + i * T), bar(B_FULLQ));
+        ++q_issued;
+      }
+      __syncwarp();
+    }
+  } else if (warp == 8) {
+    // ===================== MMA issue (one lane) =====================
+    // Step u of a segment belongs to softmax group u & 1 and key tile u / 2 (two
+    // Q tiles) or u; the order is S(0), S(1), then per step O(u), S(u + 2).
+    if (lane == 0) {
+      const uint64_t dq = smem_desc(sb, 16, 1024);
+      const uint64_t dk = smem_desc(sb + Gm::kOffRing, 16, 1024);
+      const uint64_t dv = smem_desc(sb + Gm::kOffRing, kBlock, 1024);
+      int steps[2] = {0, 0};                 // steps of each group so far
+      int base = 0;                          // ring position of the segment's first tile
+      for (int nd = 0;; ++nd) {
+        const int slot = nd & 1;
+        if (!mbar_wait(bar(B_IFULL + slot), (nd >> 1) & 1, &s_abort)) break;
+        const Segment sg = s_seg[slot];
+        mbar_arrive(bar(B_IEMPTY + slot));
+        if (sg.b < 0) break;
+        const int n = sg.n_tiles, two = sg.two, U = two ? 2 * n : n;
+        if (!mbar_wait(bar(B_FULLQ), nd & 1, &s_abort)) break;
+        auto issue_s = [&](int u) {
+          const int g = u & 1, r = base + seq_k(two ? u >> 1 : u);
+          const int s = r % kStages;
+          if (!mbar_wait(bar(B_FULL + s), (r / kStages) & 1, &s_abort)) return false;
+          tc_fence_after();
+          const uint64_t kd = dk + (uint64_t)(s * kTileBytes >> 4);
+          const uint64_t qd = dq + (uint64_t)((two && g ? kTileBytes : 0) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < kD / 16; ++ks) {
+            const uint64_t off = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
+            mma_ss(tmem + g * 128, qd + off, kd + off, kIdS, ks > 0);
+          }
+          tc_commit(bar(B_SDONE + g));
+          if (!two || g) tc_commit(bar(B_EMPTY + s));
+          if (u == U - 1) tc_commit(bar(B_QFREE));
+          return true;
+        };
+        bool ok = issue_s(0);
+        if (ok && U > 1) ok = issue_s(1);
+        for (int u = 0; u < U && ok; ++u) {
+          const int g = u & 1, t = two ? u >> 1 : u;
+          const int r = base + seq_v(t, n), s = r % kStages;
+          if (!(ok = mbar_wait(bar(B_FULL + s), (r / kStages) & 1, &s_abort))) break;
+          if (!(ok = mbar_wait(bar(B_PREADY + g), steps[g] & 1, &s_abort))) break;
+          ++steps[g];
+          tc_fence_after();
+          const uint64_t vd = dv + (uint64_t)(s * kTileBytes >> 4);
+#pragma unroll
+          for (int ks = 0; ks < kKeys / 16; ++ks)
+            mma_ts(tmem + 256 + g * kD, tmem + g * 128 + ks * 8,
+                   vd + (uint64_t)(ks * 16 * 128 >> 4), kIdO, (u >= 2 || ks > 0) ? 1u : 0u);
+          if (!two || g) tc_commit(bar(B_EMPTY + s));
+          if (u + 2 >= U) tc_commit(bar(B_ODONE + g));
+          else ok = issue_s(u + 2);
+        }
+        if (!ok) break;
+        if (U == 1) tc_commit(bar(B_ODONE + 1));
+        base += 2 * n;
+      }
+    }
+  } else if (warp < 8) {
+    // ===================== softmax group =====================
+    const int grp = warp >> 2;
+    const int r = tid & 127;                 // row of the Q tile = TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + grp * 128 + lane_off;
+    const uint32_t tO = tmem + 256 + grp * kD + lane_off;
+    const int head = kvh * G + r % G;
+    const float sg2 = P.sinks && r < TG ? P.sinks[head] * 1.4426950408889634f : -INFINITY;
+    const float sc = P.scale_log2;
+    const uint64_t sc2 = f2pack(sc, sc);
+    int steps = 0, joins = 0;
+    for (int nd = 0;; ++nd) {
+      const int slot = nd & 1;
+      if (!wait_all(bar(B_IFULL + slot), (nd >> 1) & 1)) break;
+      const Segment sg = s_seg[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
+      if (sg.b < 0) break;
+      const int two = sg.two;
+      const int tr = (two ? grp * T : 0) + r / G;      // node of the item
+      const bool row_valid = r < TG && tr < sg.n_tok;
+      const bool any_row = __any_sync(0xffffffffu, row_valid);
+      const uint32_t *row = P.tree.mask + (sg.q0 + (row_valid ? tr : 0)) * P.tree.words;
+      int64_t lo_row = 0;
+      if (row_valid) {
+        const int depth = P.tree.depth[sg.q0 + tr];
+        lo_row = tree_first_col(first_position(P.kind, P.window, sg.prefix + depth), sg.prefix,
+                                sg.n0 + tr, depth, row);
+      }
+      float m_run = row_valid ? -INFINITY : 0.f, l_run = 0.f;
+      bool alive = true, first = true;
+      for (int t = two ? 0 : grp; t < sg.n_tiles; t += two ? 1 : 2) {
+        if (!wait_all(bar(B_SDONE + grp), steps & 1)) {
+          alive = false;
+          break;
+        }
+        ++steps;
+        tc_fence_after();
+        uint64_t acc2[2] = {0ull, 0ull};
+#pragma unroll 1
+        for (int cb = 0; any_row && cb < 2; ++cb) {
+          const int64_t c0 = sg.col0 + (int64_t)t * kKeys + cb * 64;   // the chunk's first column
+          // Columns of the chunk this row reads.
+          const bool edge = row_valid && !(c0 >= lo_row && c0 + 64 <= sg.prefix);
+          uint64_t allow = row_valid ? ~0ull : 0ull;
+          const bool any_edge = __any_sync(0xffffffffu, edge);
+          if (any_edge) {
+            if (edge)
+              allow = bit_range(lo_row - c0, sg.prefix - c0) |
+                      (c0 + 64 > sg.prefix ? row_bits(row, P.tree.words, c0 - sg.prefix) &
+                                                 bit_range(max(lo_row, sg.prefix) - c0, 64)
+                                           : 0ull);
+            if (!__any_sync(0xffffffffu, allow != 0ull)) {
+              uint32_t zero[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) zero[e] = 0u;
+              TC_ST32(tS + cb * 32, zero);
+              continue;
+            }
+          }
+          uint32_t rr[64];
+          TC_LD32(tS + cb * 64, rr);
+          TC_LD32(tS + cb * 64 + 32, (rr + 32));
+          tc_wait_ld();
+          if (any_edge) {
+            const uint32_t a0 = (uint32_t)allow, a1 = (uint32_t)(allow >> 32);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (!(a0 >> e & 1u)) rr[e] = 0xff800000u;
+              if (!(a1 >> e & 1u)) rr[32 + e] = 0xff800000u;
+            }
+          }
+          // The exponentials are taken against the row's reference maximum; the
+          // chunk's own maximum is computed only for a row's first chunk and
+          // when the weights' sum shows that a score outgrew the reference.
+          // Raising the reference rescales what was summed against the old one.
+          bool redo = __any_sync(0xffffffffu, m_run == -INFINITY);
+          uint32_t pk[32];
+          uint64_t c2[2];
+#pragma unroll 1
+          for (int pass = 0;; ++pass) {
+            if (redo) {
+              float m2[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int e = 0; e < 64; e += 2)
+                m2[(e >> 1) & 3] =
+                    max3(m2[(e >> 1) & 3], __uint_as_float(rr[e]), __uint_as_float(rr[e + 1]));
+              float cm = max3(m2[0], m2[1], fmaxf(m2[2], m2[3]));
+              cm = cm == -INFINITY ? -INFINITY : cm * sc;
+              float corr = 1.f;
+              if (row_valid &&
+                  (cm > m_run + kRescaleGap || (m_run == -INFINITY && cm != -INFINITY))) {
+                corr = m_run == -INFINITY ? 1.f : exp2f(m_run - cm);
+                m_run = cm;
+              }
+              if (__any_sync(0xffffffffu, corr != 1.f)) {
+                if (!first) {
+#pragma unroll 1
+                  for (int ob = 0; ob < kD / 32; ++ob) {
+                    uint32_t ro[32];
+                    TC_LD32(tO + ob * 32, ro);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                      ro[e] = __float_as_uint(__uint_as_float(ro[e]) * corr);
+                    TC_ST32(tO + ob * 32, ro);
+                  }
+                }
+                if (cb == 1) {
+                  uint32_t pp[32];
+                  tc_wait_st();
+                  TC_LD32(tS, pp);
+                  tc_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) {
+                    const float2 f = unpack_p<false>(pp[e]);
+                    pp[e] = pack_p<false>(f.x * corr, f.y * corr);
+                  }
+                  TC_ST32(tS, pp);
+                }
+                float a0, a1, b0, b1;
+                f2unpack(acc2[0], a0, a1);
+                f2unpack(acc2[1], b0, b1);
+                acc2[0] = f2pack(a0 * corr, a1 * corr);
+                acc2[1] = f2pack(b0 * corr, b1 * corr);
+                l_run *= corr;
+              }
+            }
+            const float mu = m_run == -INFINITY ? 0.f : m_run;
+            const uint64_t nmu2 = f2pack(-mu, -mu);
+            c2[0] = c2[1] = 0ull;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float t0, t1;
+              f2unpack(fma2(f2pack(__uint_as_float(rr[2 * e]), __uint_as_float(rr[2 * e + 1])), sc2,
+                            nmu2),
+                       t0, t1);
+              const float a0 = ex2(t0), a1 = ex2(t1);
+              c2[e & 1] = add2(c2[e & 1], f2pack(a0, a1));
+              pk[e] = pack_p<false>(a0, a1);
+            }
+            if (pass == 1) break;
+            float s0, s1, s2, s3;
+            f2unpack(c2[0], s0, s1);
+            f2unpack(c2[1], s2, s3);
+            redo = __any_sync(0xffffffffu, row_valid && (s0 + s1) + (s2 + s3) > kSumCap);
+            if (!redo) break;
+          }
+          acc2[0] = add2(acc2[0], c2[0]);
+          acc2[1] = add2(acc2[1], c2[1]);
+          TC_ST32(tS + cb * 32, pk);
+        }
+        {
+          float s0, s1, s2, s3;
+          f2unpack(acc2[0], s0, s1);
+          f2unpack(acc2[1], s2, s3);
+          l_run += (s0 + s1) + (s2 + s3);
+        }
+        first = false;
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(B_PREADY + grp));
+      }
+      if (!alive) break;
+      // ---- epilogue ----
+      if (!wait_all(bar(B_ODONE + grp), nd & 1)) break;
+      float w0 = 1.f, w1 = 0.f;              // weights of this group's and the other's O
+      if (!two) {
+        // Join the groups' halves of the keys: row statistics through shared
+        // memory, accumulators read from TMEM; group i writes half i of D.
+        s_stat[grp * kTileRows + r] = make_float2(m_run, l_run);
+        mbar_arrive(bar(B_STAT));
+        if (!wait_all(bar(B_STAT), joins & 1)) break;
+        if (!wait_all(bar(B_ODONE + (grp ^ 1)), nd & 1)) break;
+        const float2 o = s_stat[(grp ^ 1) * kTileRows + r];
+        const float m = fmaxf(m_run, o.x);
+        w0 = m_run == -INFINITY ? 0.f : exp2f(m_run - m);
+        w1 = o.x == -INFINITY ? 0.f : exp2f(o.x - m);
+        m_run = m;
+        l_run = l_run * w0 + o.y * w1;
+      }
+      tc_fence_after();
+      float f = 1.f;
+      if (sg.part < 0) {
+        const float mr = m_run == -INFINITY ? 0.f : m_run;
+        const float mfin = fmaxf(mr, sg2);
+        const float rsc = exp2f(mr - mfin);
+        const float denom = l_run * rsc + (P.sinks ? exp2f(sg2 - mfin) : 0.f);
+        f = denom > 0.f ? rsc / denom : 0.f;
+      }
+      w0 *= f;
+      w1 *= f;
+      const int row_i = (two ? grp * TG : 0) + r;      // row of the item
+      float *part = sg.part < 0 ? nullptr
+                                : P.partials + ((int64_t)blockIdx.x * 2 + sg.part) * P.part_stride;
+      const int rows_max = (int)(P.part_stride / (kD + 2));
+      if (part && row_valid && (two || grp == 0))
+        reinterpret_cast<float2 *>(part + (int64_t)rows_max * kD)[row_i] = make_float2(m_run, l_run);
+      __nv_bfloat16 *orow = P.out + ((sg.q0 + tr) * (int64_t)(P.hkv * G) + head) * kD;
+      const int d_lo = two ? 0 : grp * (kD / 2), d_hi = two ? kD : d_lo + kD / 2;
+      const uint32_t tO2 = tmem + 256 + (grp ^ 1) * kD + lane_off;
+      __syncwarp();
+#pragma unroll 1
+      for (int d = d_lo; any_row && d < d_hi; d += 32) {
+        uint32_t a[32];
+        TC_LD32(tO + d, a);
+        if (two) {
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * w0);
+        } else {
+          uint32_t b[32];
+          TC_LD32(tO2 + d, b);
+          tc_wait_ld();
+          // An accumulator without weight may hold anything.
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float x = w0 != 0.f ? __uint_as_float(a[e]) * w0 : 0.f;
+            a[e] = __float_as_uint(w1 != 0.f ? fmaf(__uint_as_float(b[e]), w1, x) : x);
+          }
+        }
+        if (part && row_valid) {
+          float4 *dst = reinterpret_cast<float4 *>(part + (int64_t)row_i * kD + d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(__uint_as_float(a[4 * e]), __uint_as_float(a[4 * e + 1]),
+                                 __uint_as_float(a[4 * e + 2]), __uint_as_float(a[4 * e + 3]));
+        } else if (row_valid) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack_p<false>(__uint_as_float(a[8 * e + 2 * k]),
+                                   __uint_as_float(a[8 * e + 2 * k + 1]));
+            *reinterpret_cast<uint4 *>(orow + d + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();   // the TMEM loads are warp-collective
+      }
+      __syncwarp();
+      if (!two) {
+        // Both groups have read both accumulators (and the statistics) before
+        // the next segment's products overwrite them.
+        tc_fence_before();
+        mbar_arrive(bar(B_EPI));
+        if (!wait_all(bar(B_EPI), joins & 1)) break;
+        tc_fence_after();
+        ++joins;
+      }
+    }
+  }
+  // Every role has left its loop: s_abort is final.
+  __syncthreads();
+  if (s_abort) {
+    // Loads and products already issued complete on their own; wait for them
+    // before the shared memory and TMEM they write are released.
+    if (tid == 0) set_error(P.err, SWA_DEVERR_TIMEOUT);
+    if (warp == 9 && lane == 0)
+      for (int s = 0; s < kStages; ++s) {
+        const int fills = (ring_issued + kStages - 1 - s) / kStages;
+        if (fills) mbar_drain(bar(B_FULL + s), (fills - 1) & 1);
+      }
+    if (warp == 10 && lane == 0 && q_issued) mbar_drain(bar(B_FULLQ), (q_issued - 1) & 1);
+    if (warp == 8 && lane == 0) {
+      tc_commit(bar(B_DRAIN));
+      mbar_drain(bar(B_DRAIN), 0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+}
+
+// Merges the partials of the items that cross CTAs: CTA (chunk, c) the rows
+// [16 chunk, 16 chunk + 16) of the item that CTA c of the main launch began and
+// left.  A warp takes a row: the contributors' maxima and sums first, then the
+// weighted sum of their output rows, in group order.
+template <int kD>
+__global__ void __launch_bounds__(kMergeThreads) k_tree_merge(const __grid_constant__ TreeParams P) {
+  constexpr int kPer = kD / 32;              // floats per lane
+  using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
+  const MergeDesc d = P.desc[blockIdx.y];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = blockIdx.y % P.hkv, G = P.G;
+  const int rows_max = (int)(P.part_stride / (kD + 2));
+  auto part = [&](int i) {
+    return P.partials +
+           (((int64_t)blockIdx.y + (int64_t)i * P.hkv) * 2 + (i == 0 ? 1 : 0)) * P.part_stride;
+  };
+  if (d.parts < 2) return;
+  for (int i = warp; i < kMergeRows; i += kMergeThreads / 32) {
+    const int r = blockIdx.x * kMergeRows + i;
+    if (r >= d.n_tok * G) break;
+    const int head = kvh * G + r % G;
+    auto stat = [&](int k) {
+      return reinterpret_cast<const float2 *>(part(k) + (int64_t)rows_max * kD)[r];
+    };
+    float mx = -INFINITY;
+    for (int k = lane; k < d.parts; k += 32) mx = fmaxf(mx, stat(k).x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float sg2 = P.sinks ? P.sinks[head] * 1.4426950408889634f : -INFINITY;
+    const float M = fmaxf(mx, sg2);
+    float L = 0.f, acc[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    for (int k0 = 0; k0 < d.parts; k0 += 32) {
+      float w = 0.f;
+      if (k0 + lane < d.parts) {
+        const float2 s = stat(k0 + lane);
+        w = s.x == -INFINITY ? 0.f : exp2f(s.x - M);
+        L += w * s.y;
+      }
+      const int m = min(32, d.parts - k0);
+#pragma unroll 4
+      for (int k = 0; k < m; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const Vec v = *reinterpret_cast<const Vec *>(part(k0 + k) + (int64_t)r * kD + lane * kPer);
+        const float *x = reinterpret_cast<const float *>(&v);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = wk != 0.f ? fmaf(x[e], wk, acc[e]) : acc[e];
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (P.sinks) L += exp2f(sg2 - M);
+    const float f = 1.f / L;
+    __nv_bfloat16 *dst =
+        P.out + ((d.q0 + r / G) * (int64_t)(P.hkv * G) + head) * kD + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2)
+      *reinterpret_cast<uint32_t *>(dst + e) = pack_p<false>(acc[e] * f, acc[e + 1] * f);
+  }
+}
+
+int tile_nodes(const Ctx &c, int layer, int max_new) {
+  return std::min(kTileRows / (c.cfg.num_q_heads / c.layers[layer].hkv), max_new);
+}
+
+struct TreeWs {
+  int groups, rows;          // CTAs per KV head; rows of an item
+  bool whole;                // items are not split
+  int64_t part_stride;       // floats
+  size_t desc_bytes, total;
+};
+
+TreeWs tree_ws(const Ctx &c, int layer, int max_new, int max_seq_len) {
+  const LayerInfo &L = c.layers[layer];
+  TreeWs w;
+  const int G = c.cfg.num_q_heads / L.hkv, T = tile_nodes(c, layer, max_new);
+  w.groups = std::max(1, (c.num_sms > 0 ? c.num_sms : 148) / L.hkv);
+  w.rows = std::min(2 * T, max_new) * G;
+  w.whole = tree_max_keys(c, layer, max_new, max_seq_len) <= 512;
+  w.part_stride = (int64_t)w.rows * (c.cfg.head_dim + 2);
+  // the statistics are read as pairs, the next partial's rows as 16-byte words
+  w.part_stride = (w.part_stride + 3) / 4 * 4;
+  w.desc_bytes = ((size_t)w.groups * L.hkv * sizeof(MergeDesc) + 255) / 256 * 256;
+  w.total = w.whole ? 256
+                    : w.desc_bytes + (size_t)w.groups * L.hkv * 2 * w.part_stride * sizeof(float);
+  return w;
+}
+
+template <int D>
+cudaError_t launch_tree(const LayerInfo &L, const CUtensorMap &tmq, const TreeParams &P, int rows,
+                        cudaStream_t s) {
+  using Gm = TreeGeo<D>;
+  const size_t smem = Gm::kOffCtl + sizeof(Control);
+  static_assert(B_COUNT == 31 && Gm::kOffCtl + sizeof(Control) <= 227 * 1024,
+                "shared memory of a CTA");
+  cudaError_t e = cudaFuncSetAttribute(k_tree_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  const int ctas = P.groups * P.hkv;
+  k_tree_tc<D><<<ctas, kTreeThreads, smem, s>>>(L.tmk, L.tmv, tmq, P);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || P.whole) return e;
+  dim3 grid((rows + kMergeRows - 1) / kMergeRows, ctas);
+  k_tree_merge<D><<<grid, kMergeThreads, 0, s>>>(P);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool tc_tree_supported(const Ctx &c, int layer) {
+  const LayerInfo &L = c.layers[layer];
+  return L.tma && c.cfg.kv_dtype == SWA_DTYPE_BF16 &&
+         (c.cfg.head_dim == 64 || c.cfg.head_dim == 128) && c.cfg.page_size <= 64;
+}
+
+size_t tc_tree_ws_bytes(const Ctx &c, int layer, int max_new, int max_seq_len) {
+  return (tree_ws(c, layer, max_new, max_seq_len).total + 255) / 256 * 256;
+}
+
+cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree, cudaStream_t s) {
+  if (a.nq == 0) return cudaSuccess;
+  const LayerInfo &L = c.layers[a.layer];
+  const TreeWs w = tree_ws(c, a.layer, a.max_new, a.max_seq_len);
+  TreeParams P{};
+  P.kind = L.kind;
+  P.window = L.window;
+  P.hkv = L.hkv;
+  P.G = c.cfg.num_q_heads / L.hkv;
+  P.T = tile_nodes(c, a.layer, a.max_new);
+  P.ps = c.cfg.page_size;
+  P.ps_shift = __builtin_ctz((unsigned)P.ps);
+  P.page_stride = (int64_t)P.ps * (L.addr.blocks ? L.addr.blocks : 1);
+  P.pool_rows = (L.in_full ? c.cfg.size_full : c.cfg.size_swa) + c.cfg.page_size;
+  P.rt = a.rt;
+  P.rt_stride = a.rt_stride;
+  P.req_idx = a.req_idx;
+  P.pre = a.pre;
+  P.qo_indptr = a.qo_indptr;
+  P.bs = a.bs;
+  P.groups = w.groups;
+  P.max_new = a.max_new;
+  P.whole = w.whole ? 1 : 0;
+  P.n_tokens = a.nq;
+  P.plan = a.plan;
+  P.tree = tree;
+  P.sinks = a.sinks;
+  P.scale_log2 = a.scale * 1.4426950408889634f;
+  P.out = static_cast<__nv_bfloat16 *>(a.out);
+  P.desc = static_cast<MergeDesc *>(a.ws);
+  P.partials = reinterpret_cast<float *>(static_cast<char *>(a.ws) + w.desc_bytes);
+  P.part_stride = w.part_stride;
+  P.err = c.err_word;
+  CUtensorMap tmq;
+  if (!make_q_tile_map(&tmq, a.q, a.nq, c.cfg.num_q_heads, c.cfg.head_dim, P.G, P.T))
+    return cudaErrorInvalidValue;
+  return c.cfg.head_dim == 64 ? launch_tree<64>(L, tmq, P, w.rows, s)
+                              : launch_tree<128>(L, tmq, P, w.rows, s);
+}
+
+}  // namespace swa

@@ -768,11 +768,16 @@ swa_status swa_tree_plan(swa_ctx *c, int32_t bs, const int32_t *parents,
   return SWA_OK;
 }
 
+static bool use_tree_tc(const swa_ctx *c, int layer) {
+  return c->forced_path == -1 && swa::tc_tree_supported(*c, layer);
+}
+
 size_t swa_attn_tree_ws_bytes(const swa_ctx *c, int32_t layer, int32_t bs, int64_t n_tokens,
                               int32_t max_new, int32_t max_seq_len) {
   if (!c || layer < 0 || layer >= c->cfg.num_layers || bs < 0 || n_tokens < 0 || max_new < 1 ||
       max_new > SWA_TREE_MAX_NODES || max_seq_len < 1)
     return 0;
+  if (use_tree_tc(c, layer)) return swa::tc_tree_ws_bytes(*c, layer, max_new, max_seq_len);
   return swa::simt_tree_ws_bytes(*c, layer, n_tokens, max_new, max_seq_len);
 }
 
@@ -798,7 +803,8 @@ swa_status swa_attn_tree(swa_ctx *c, int32_t layer, int32_t bs, const int32_t *r
     return fail(c, SWA_ERR_INVALID, "q and out must be 16-byte aligned");
   if (!ws || ws_bytes < swa_attn_tree_ws_bytes(c, layer, bs, n_tokens, max_new, max_seq_len))
     return fail(c, SWA_ERR_INVALID, "split workspace too small");
-  if (n_tokens > 65535)
+  const bool tc = use_tree_tc(c, layer);
+  if (n_tokens > (tc ? 0x7fffffff : 65535))
     return fail(c, SWA_ERR_INVALID, "n_tokens > 65535 on the generic path");
   swa::AttnArgs a{};
   a.layer = layer;
@@ -821,8 +827,9 @@ swa_status swa_attn_tree(swa_ctx *c, int32_t layer, int32_t bs, const int32_t *r
   a.ws = ws;
   a.ws_bytes = ws_bytes;
   const swa::TreeView tv = swa::tree_view(tree, n_tokens, max_new);
-  c->last_path = 0;
-  CUDA_TRY(c, swa::launch_attn_tree_simt(*c, a, tv, (cudaStream_t)stream));
+  c->last_path = tc ? 3 : 0;
+  if (tc) CUDA_TRY(c, swa::launch_attn_tree_tc(*c, a, tv, (cudaStream_t)stream));
+  else CUDA_TRY(c, swa::launch_attn_tree_simt(*c, a, tv, (cudaStream_t)stream));
   return SWA_OK;
 }
 

@@ -68,6 +68,16 @@ int64_t tree_max_keys(const Ctx &c, int layer, int max_new, int max_seq_len);
 size_t simt_tree_ws_bytes(const Ctx &c, int layer, int64_t nq, int max_new, int max_seq_len);
 cudaError_t launch_attn_tree_simt(Ctx &c, const AttnArgs &a, const TreeView &tree, cudaStream_t s);
 
+// ---- tma.cu -------------------------------------------------------------------
+// TMA tensor map over queries x [nq][hq][d] (bf16) whose box is one tile of t
+// tokens x g heads, 64 dims wide.  False as for make_qo_tensor_map.
+bool make_q_tile_map(CUtensorMap *m, const void *x, int64_t nq, int hq, int d, int g, int t);
+
+// ---- attn_tree_tc.cu ------------------------------------------------------------
+bool tc_tree_supported(const Ctx &c, int layer);
+size_t tc_tree_ws_bytes(const Ctx &c, int layer, int max_new, int max_seq_len);
+cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree, cudaStream_t s);
+
 // ---- qk_norm_rope.cu ----------------------------------------------------------
 struct QkNormArgs {
   const void *q, *k, *v;

@@ -11,6 +11,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "spec_internal.h"
 #include "swa_internal.h"
 
 namespace swa {
@@ -65,16 +66,20 @@ void make_kv_tensor_maps(Ctx &c, int layer) {
   L.tma = true;
 }
 
-bool make_qo_tensor_map(CUtensorMap *m, const void *x, int64_t nq, int hq, int d, int g) {
+bool make_q_tile_map(CUtensorMap *m, const void *x, int64_t nq, int hq, int d, int g, int t) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (!fn || nq <= 0 || ((uintptr_t)x & 15) || g <= 0 || g > 128) return false;
+  if (!fn || nq <= 0 || ((uintptr_t)x & 15) || g <= 0 || t <= 0 || g * t > 128) return false;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)hq, (cuuint64_t)nq};
   cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)hq * d * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)g, (cuuint32_t)(128 / g)};
+  cuuint32_t box[3] = {64, (cuuint32_t)g, (cuuint32_t)t};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(x), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_qo_tensor_map(CUtensorMap *m, const void *x, int64_t nq, int hq, int d, int g) {
+  return g > 0 && make_q_tile_map(m, x, nq, hq, d, g, 128 / g);
 }
 
 }  // namespace swa

@@ -382,3 +382,16 @@ def test_device_checks():
     for l in range(2):
         S.check(l, what="after device checks")
     assert api.swa_device_check(P.ctx) == 0
+
+
+@pytest.mark.parametrize("shape,ps,kernel", [(MIMO, 64, 3), (MIMO, 16, 3), (MIMO, 1, 0), (GPTOSS, 32, 3),
+                                             (TINY, 1, 0)],
+                         ids=["mimo-ps64", "mimo-ps16", "mimo-ps1", "gptoss", "tiny"])
+def test_kernel_taken(shape, ps, kernel):
+    """The tensor-core kernel serves bf16 pages of 16 to 64; -1 and 0 select."""
+    P, S = _step(shape, ps, [40], [[-1, 0, 0]])
+    S.attend(1)
+    assert api.swa_last_attn_path(P.ctx) == kernel
+    api.swa_set_attn_path(P.ctx, 0)
+    S.attend(1)
+    assert api.swa_last_attn_path(P.ctx) == 0
