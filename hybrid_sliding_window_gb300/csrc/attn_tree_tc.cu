@@ -1,5 +1,6 @@
 // Draft-tree attention on the 5th-generation tensor cores (tcgen05 + TMEM + TMA):
-// bf16 KV with D = 64 or 128, any GQA group, page size 16..64.
+// bf16 KV with D = 64 or 128, or E4M3 KV with D = 128; any GQA group, page size
+// 16..64.
 //
 // Method: node i of a request reads the cached columns of its window and its
 // ancestors' columns behind the prefix (include/swa.h, swa_attn_tree).  With T
@@ -29,7 +30,7 @@
 //     looks page rows up 32 page slots at a time and streams K and V tiles by
 //     TMA through one ring, in the order in which the MMAs use them;
 //   * warp 10 loads each segment's Q tiles once the previous segment's last
-//     QK^T has read them;
+//     QK^T has read them (E4M3 KV: and converts, below);
 //   * warp 8 (one lane) issues S = Q K^T and O += P V with P in TMEM over S;
 //   * warps 0-3 and 4-7 are two softmax groups.  Rows of an item that fill two
 //     Q tiles: one tile each, both read the same key tiles.  Rows that fit one
@@ -37,6 +38,11 @@
 //     that one group's softmax overlaps the other's products, and the two
 //     accumulators are joined in TMEM's own lanes at the segment's end (warps i
 //     and i + 4 can read the same lanes).
+// E4M3 KV: K and V tiles arrive as bytes in a ring of their own; warps 10 and 11
+// turn them into f16 tiles (exact: E4M3 is a subset of f16) and each Q tile,
+// which they also load, from bf16 to f16 in place (12 warps in all: a 13th would
+// cost every thread a quarter of its registers); the products run on f16 operands, P is packed as f16,
+// the K scale joins the softmax scale and the V scale the output.
 // Key columns that some row may not read (window edge, non-ancestors) get -inf
 // scores from a 64-bit mask per row and 64-column chunk; chunks that no row of
 // a warp reads are skipped.
@@ -61,19 +67,24 @@ constexpr int kTileRows = 128;               // rows of a Q tile (M)
 constexpr int kKeys = 128;                   // keys of a K/V tile
 constexpr int kBlock = kTileRows * 64 * 2;   // one 64-column block of a tile
 constexpr int kTreeThreads = 352;            // 8 softmax warps, MMA, producer, Q loader
+constexpr int kConvThreads = 64;             // E4M3 KV: warps 10 and 11 convert
 constexpr float kRescaleGap = 8.f;           // log2 units: rescale O when the max grows more
 constexpr float kSumCap = 32768.f;           // a chunk's weight sum that forces a maximum pass
 constexpr int kMergeThreads = 128;
 constexpr int kMergeRows = 16;               // rows of one merge CTA
 
-template <int D>
+template <int D, bool F8>
 struct TreeGeo {
   static constexpr int kTileBytes = kKeys * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = F8 ? 3 : D == 128 ? 5 : 8;   // operand tiles
+  static constexpr int kRawBytes = kKeys * D;                 // E4M3 tiles as loaded
+  static constexpr int kRawStages = F8 ? 4 : 0;
   static constexpr int kOffRing = 2 * kTileBytes;             // after the Q tiles
-  static constexpr int kOffStat = kOffRing + kStages * kTileBytes;
+  static constexpr int kOffRaw = kOffRing + kStages * kTileBytes;
+  static constexpr int kOffStat = kOffRaw + kRawStages * kRawBytes;
   static constexpr int kOffBars = kOffStat + 2 * kTileRows * 8;
-  static constexpr int kOffCtl = kOffBars + 31 * 8 + 8;       // Control
+  static constexpr int kOffCtl = kOffBars + 40 * 8;           // Control
+  static constexpr int kThreads = F8 ? 384 : kTreeThreads;
 };
 
 struct TreeParams {
@@ -88,7 +99,8 @@ struct TreeParams {
   PlanView plan;
   TreeView tree;
   const float *sinks;
-  float scale_log2;
+  float scale_log2;          // E4M3 KV: with the K scale
+  float v_scale;             // 1 unless E4M3 KV
   __nv_bfloat16 *out;
   float *partials;           // [CTA][2][rows x D, then rows x 2]
   int64_t part_stride;       // floats of one partial
@@ -121,7 +133,7 @@ struct Control {
 
 enum { B_IFULL = 0, B_IEMPTY = 2, B_FULLQ = 4, B_QFREE = 5, B_SDONE = 6, B_PREADY = 8,
        B_ODONE = 10, B_STAT = 12, B_EPI = 13, B_DRAIN = 14, B_FULL = 15, B_EMPTY = 23,
-       B_COUNT = 31 };
+       B_RAWFULL = 31, B_RAWEMPTY = 35, B_QCONV = 39, B_COUNT = 40 };
 
 // Position in the ring of key tile i's K or V, of the n tiles of a segment: K0
 // K1 V0 K2 V1 ... - the order in which the products release them.
@@ -196,13 +208,25 @@ __device__ __forceinline__ uint64_t row_bits(const uint32_t *row, int words, int
   return (uint64_t)__funnelshift_r(x[0], x[1], s) | (uint64_t)__funnelshift_r(x[1], x[2], s) << 32;
 }
 
-template <int kD>
-__global__ void __launch_bounds__(kTreeThreads, 1)
+// (row r, 16-byte chunk c) of an operand tile: blocks of [128 rows][128 B] with the
+// 128-byte swizzle.
+__device__ __forceinline__ int tile_off(int r, int c) {
+  return (c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+template <int kD, bool kF8>
+__global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     k_tree_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
               const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TreeParams P) {
-  using Gm = TreeGeo<kD>;
+  using Gm = TreeGeo<kD, kF8>;
+  static_assert(!kF8 || kD == 128, "E4M3 KV: D = 128");
   constexpr int kTileBytes = Gm::kTileBytes, kStages = Gm::kStages;
   static_assert(kStages <= 8, "barrier slots");
+  // The ring that TMA fills: the operand tiles, or the E4M3 bytes.
+  constexpr int kLoads = kF8 ? Gm::kRawStages : kStages;
+  constexpr int kLoadBytes = kF8 ? Gm::kRawBytes : kTileBytes;
+  constexpr int kOffLoad = kF8 ? Gm::kOffRaw : Gm::kOffRing;
+  constexpr int bLoadFull = kF8 ? B_RAWFULL : B_FULL, bLoadEmpty = kF8 ? B_RAWEMPTY : B_EMPTY;
   extern __shared__ __align__(1024) char smem[];
   const uint32_t sb = smem_u32(smem);
   float2 *s_stat = reinterpret_cast<float2 *>(smem + Gm::kOffStat);   // [group][row] max, sum
@@ -234,7 +258,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_IFULL + i), 1);
-      mbar_init(bar(B_IEMPTY + i), 10);   // 8 softmax warps, the MMA lane, the Q loader
+      // 8 softmax warps, the MMA lane, the Q loader (or two converters)
+      mbar_init(bar(B_IEMPTY + i), kF8 ? 11 : 10);
       mbar_init(bar(B_SDONE + i), 1);
       mbar_init(bar(B_PREADY + i), kTileRows);
       mbar_init(bar(B_ODONE + i), 1);
@@ -245,19 +270,41 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     mbar_init(bar(B_EPI), 2 * kTileRows);
     mbar_init(bar(B_DRAIN), 1);
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(B_FULL + i), 1);
+      mbar_init(bar(B_FULL + i), kF8 ? kConvThreads : 1);
       mbar_init(bar(B_EMPTY + i), 1);
     }
+    for (int i = 0; i < Gm::kRawStages; ++i) {
+      mbar_init(bar(B_RAWFULL + i), 1);
+      mbar_init(bar(B_RAWEMPTY + i), 2);
+    }
+    mbar_init(bar(B_QCONV), kConvThreads);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-  constexpr uint32_t kIdS = idesc_f16(128, 128, false);
-  constexpr uint32_t kIdO = idesc_f16(128, kD, true);
+  constexpr uint32_t kIdS = idesc_f16(128, 128, false, kF8);
+  constexpr uint32_t kIdO = idesc_f16(128, kD, true, kF8);
 
   // Loads issued, for the abort path: ring slots filled (producer), Q fills.
   int ring_issued = 0, q_issued = 0;
+
+  // Warp-collective, warp 10: the Q tiles of the CTA's segment nd, once the last
+  // QK^T of the one before has read the buffers.
+  auto load_q = [&](const Segment &sg, int nd) {
+    if (nd >= 1 && !wait_all(bar(B_QFREE), (nd - 1) & 1)) return false;
+    if (lane == 0) {
+      const int tiles = sg.two ? 2 : 1;
+      mbar_expect_tx(bar(B_FULLQ), (uint32_t)(tiles * TG * 128 * (kD / 64)));
+      for (int i = 0; i < tiles; ++i)
+        for (int h = 0; h < kD / 64; ++h)
+          tma_load_3d(sb + i * kTileBytes + h * kBlock, &tmQ, h * 64, kvh * G,
+                      (int)(sg.q0 + i * T), bar(B_FULLQ));
+      ++q_issued;
+    }
+    __syncwarp();
+    return true;
+  };
 
   if (warp == 9) {
     // ===================== producer: segments, K/V tiles =====================
@@ -313,14 +360,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         int good = 1;
         if (lane == 0) {
-          const int s = ring_issued % kStages, f = ring_issued / kStages;
-          if (f >= 1) good = mbar_wait(bar(B_EMPTY + s), (f - 1) & 1, &s_abort);
+          const int s = ring_issued % kLoads, f = ring_issued / kLoads;
+          if (f >= 1) good = mbar_wait(bar(bLoadEmpty + s), (f - 1) & 1, &s_abort);
           if (good) {
             const int32_t *rows = &s_rows[(i0 >> 5) & 1][i0 & 31];
-            const uint32_t dst = sb + Gm::kOffRing + s * kTileBytes, full = bar(B_FULL + s);
-            mbar_expect_tx(full, (uint32_t)kTileBytes);
+            const uint32_t dst = sb + kOffLoad + s * kLoadBytes, full = bar(bLoadFull + s);
+            mbar_expect_tx(full, (uint32_t)kLoadBytes);
             for (int i = 0; i < ppt; ++i)
-              for (int h = 0; h < kD / 64; ++h)
+              for (int h = 0; h < (kF8 ? 1 : kD / 64); ++h)
                 tma_load_3d(dst + h * kBlock + (i << P.ps_shift) * 128, is_v ? &tmV : &tmK, h * 64,
                             kvh, rows[i], full);
             ++ring_issued;
@@ -401,26 +448,80 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       end.b = -1;
       publish(end);
     }
-  } else if (warp == 10) {
-    // ===================== Q tiles =====================
-    for (int nd = 0;; ++nd) {
-      const int slot = nd & 1;
-      if (!wait_all(bar(B_IFULL + slot), (nd >> 1) & 1)) break;
-      const Segment sg = s_seg[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
-      if (sg.b < 0) break;
-      if (nd >= 1 && !wait_all(bar(B_QFREE), (nd - 1) & 1)) break;
-      if (lane == 0) {
-        const int tiles = sg.two ? 2 : 1;
-        mbar_expect_tx(bar(B_FULLQ), (uint32_t)(tiles * TG * 128 * (kD / 64)));
-        for (int i = 0; i < tiles; ++i)
-          for (int h = 0; h < kD / 64; ++h)
-            tma_load_3d(sb + i * kTileBytes + h * kBlock, &tmQ, h * 64, kvh * G,
-                        (int)(sg.q0 + i * T), bar(B_FULLQ));
-        ++q_issued;
+  } else if (warp >= 10) {
+    if constexpr (!kF8) {
+      // ===================== Q tiles =====================
+      for (int nd = 0;; ++nd) {
+        const int slot = nd & 1;
+        if (!wait_all(bar(B_IFULL + slot), (nd >> 1) & 1)) break;
+        const Segment sg = s_seg[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
+        if (sg.b < 0 || !load_q(sg, nd)) break;
       }
-      __syncwarp();
+    } else {
+      // ============ converters (E4M3 KV): Q, K and V to f16 ============
+      const int ct = tid - 320;              // 0 .. 63
+      int pos = 0;                           // ring position, both rings
+      bool ok = true;
+      for (int nd = 0; ok; ++nd) {
+        const int slot = nd & 1;
+        if (!wait_all(bar(B_IFULL + slot), (nd >> 1) & 1)) break;
+        const Segment sg = s_seg[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
+        if (sg.b < 0 || (warp == 10 && !load_q(sg, nd))) break;
+        if (!wait_all(bar(B_FULLQ), nd & 1)) break;
+        const int q_chunks = (sg.two ? 2 : 1) * kTileBytes / 16;
+#pragma unroll 4
+        for (int i = ct; i < q_chunks; i += kConvThreads) {
+          uint4 *q16 = reinterpret_cast<uint4 *>(smem + i * 16);
+          uint4 v = *q16;
+          v.x = bf16x2_to_f16x2(v.x);
+          v.y = bf16x2_to_f16x2(v.y);
+          v.z = bf16x2_to_f16x2(v.z);
+          v.w = bf16x2_to_f16x2(v.w);
+          *q16 = v;
+        }
+        fence_async_smem();                  // read by the tensor core (the async proxy)
+        mbar_arrive(bar(B_QCONV));
+        for (int j = 0; j < 2 * sg.n_tiles; ++j, ++pos) {
+          const int rs = pos % kLoads, s = pos % kStages;
+          if (!(ok = wait_all(bar(B_RAWFULL + rs), (pos / kLoads) & 1))) break;
+          if (pos >= kStages && !(ok = wait_all(bar(B_EMPTY + s), (pos / kStages - 1) & 1))) break;
+          const char *src = smem + Gm::kOffRaw + rs * Gm::kRawBytes;
+          char *dst = smem + Gm::kOffRing + s * kTileBytes;
+          // Eight lanes take chunks 0-3 of an even row and 4-7 of the next (then
+          // the other halves): neither the reads of 16 E4M3 values nor the two
+          // 16-byte writes that they become meet in a bank.
+          const int odd = (ct >> 2) & 1;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = ((h ^ odd) << 2) + (ct & 3);
+            uint4 w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = 2 * (i * 8 + (ct >> 3)) + odd;
+              w[i] = *reinterpret_cast<const uint4 *>(src + r * 128 + ((c ^ (r & 7)) << 4));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = 2 * (i * 8 + (ct >> 3)) + odd;
+              uint4 a, b;
+              e4m3x4_to_f16x4(w[i].x, a.x, a.y);
+              e4m3x4_to_f16x4(w[i].y, a.z, a.w);
+              e4m3x4_to_f16x4(w[i].z, b.x, b.y);
+              e4m3x4_to_f16x4(w[i].w, b.z, b.w);
+              *reinterpret_cast<uint4 *>(dst + tile_off(r, 2 * c)) = a;
+              *reinterpret_cast<uint4 *>(dst + tile_off(r, 2 * c + 1)) = b;
+            }
+          }
+          fence_async_smem();
+          mbar_arrive(bar(B_FULL + s));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_RAWEMPTY + rs));
+        }
+      }
     }
   } else if (warp == 8) {
     // ===================== MMA issue (one lane) =====================
@@ -439,7 +540,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         mbar_arrive(bar(B_IEMPTY + slot));
         if (sg.b < 0) break;
         const int n = sg.n_tiles, two = sg.two, U = two ? 2 * n : n;
-        if (!mbar_wait(bar(B_FULLQ), nd & 1, &s_abort)) break;
+        if (!mbar_wait(bar(kF8 ? B_QCONV : B_FULLQ), nd & 1, &s_abort)) break;
         auto issue_s = [&](int u) {
           const int g = u & 1, r = base + seq_k(two ? u >> 1 : u);
           const int s = r % kStages;
@@ -596,8 +697,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                   tc_wait_ld();
 #pragma unroll
                   for (int e = 0; e < 32; ++e) {
-                    const float2 f = unpack_p<false>(pp[e]);
-                    pp[e] = pack_p<false>(f.x * corr, f.y * corr);
+                    const float2 f = unpack_p<kF8>(pp[e]);
+                    pp[e] = pack_p<kF8>(f.x * corr, f.y * corr);
                   }
                   TC_ST32(tS, pp);
                 }
@@ -620,7 +721,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                        t0, t1);
               const float a0 = ex2(t0), a1 = ex2(t1);
               c2[e & 1] = add2(c2[e & 1], f2pack(a0, a1));
-              pk[e] = pack_p<false>(a0, a1);
+              pk[e] = pack_p<kF8>(a0, a1);
             }
             if (pass == 1) break;
             float s0, s1, s2, s3;
@@ -669,7 +770,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const float mfin = fmaxf(mr, sg2);
         const float rsc = exp2f(mr - mfin);
         const float denom = l_run * rsc + (P.sinks ? exp2f(sg2 - mfin) : 0.f);
-        f = denom > 0.f ? rsc / denom : 0.f;
+        f = denom > 0.f ? rsc / denom * P.v_scale : 0.f;
       }
       w0 *= f;
       w1 *= f;
@@ -740,9 +841,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // before the shared memory and TMEM they write are released.
     if (tid == 0) set_error(P.err, SWA_DEVERR_TIMEOUT);
     if (warp == 9 && lane == 0)
-      for (int s = 0; s < kStages; ++s) {
-        const int fills = (ring_issued + kStages - 1 - s) / kStages;
-        if (fills) mbar_drain(bar(B_FULL + s), (fills - 1) & 1);
+      for (int s = 0; s < kLoads; ++s) {
+        const int fills = (ring_issued + kLoads - 1 - s) / kLoads;
+        if (fills) mbar_drain(bar(bLoadFull + s), (fills - 1) & 1);
       }
     if (warp == 10 && lane == 0 && q_issued) mbar_drain(bar(B_FULLQ), (q_issued - 1) & 1);
     if (warp == 8 && lane == 0) {
@@ -809,7 +910,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_tree_merge(const __grid_const
 #pragma unroll
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if (P.sinks) L += exp2f(sg2 - M);
-    const float f = 1.f / L;
+    const float f = P.v_scale / L;
     __nv_bfloat16 *dst =
         P.out + ((d.q0 + r / G) * (int64_t)(P.hkv * G) + head) * kD + lane * kPer;
 #pragma unroll
@@ -845,18 +946,18 @@ TreeWs tree_ws(const Ctx &c, int layer, int max_new, int max_seq_len) {
   return w;
 }
 
-template <int D>
+template <int D, bool F8>
 cudaError_t launch_tree(const LayerInfo &L, const CUtensorMap &tmq, const TreeParams &P, int rows,
                         cudaStream_t s) {
-  using Gm = TreeGeo<D>;
+  using Gm = TreeGeo<D, F8>;
   const size_t smem = Gm::kOffCtl + sizeof(Control);
-  static_assert(B_COUNT == 31 && Gm::kOffCtl + sizeof(Control) <= 227 * 1024,
+  static_assert(B_COUNT == 40 && Gm::kOffCtl + sizeof(Control) <= 227 * 1024,
                 "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(k_tree_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(k_tree_tc<D, F8>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int ctas = P.groups * P.hkv;
-  k_tree_tc<D><<<ctas, kTreeThreads, smem, s>>>(L.tmk, L.tmv, tmq, P);
+  k_tree_tc<D, F8><<<ctas, Gm::kThreads, smem, s>>>(L.tmk, L.tmv, tmq, P);
   e = cudaGetLastError();
   if (e != cudaSuccess || P.whole) return e;
   dim3 grid((rows + kMergeRows - 1) / kMergeRows, ctas);
@@ -868,8 +969,10 @@ cudaError_t launch_tree(const LayerInfo &L, const CUtensorMap &tmq, const TreePa
 
 bool tc_tree_supported(const Ctx &c, int layer) {
   const LayerInfo &L = c.layers[layer];
-  return L.tma && c.cfg.kv_dtype == SWA_DTYPE_BF16 &&
-         (c.cfg.head_dim == 64 || c.cfg.head_dim == 128) && c.cfg.page_size <= 64;
+  const int d = c.cfg.head_dim;
+  return L.tma && c.cfg.page_size <= 64 &&
+         ((c.cfg.kv_dtype == SWA_DTYPE_BF16 && (d == 64 || d == 128)) ||
+          (c.cfg.kv_dtype == SWA_DTYPE_E4M3 && d == 128));
 }
 
 size_t tc_tree_ws_bytes(const Ctx &c, int layer, int max_new, int max_seq_len) {
@@ -903,7 +1006,9 @@ cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree,
   P.plan = a.plan;
   P.tree = tree;
   P.sinks = a.sinks;
-  P.scale_log2 = a.scale * 1.4426950408889634f;
+  const bool f8 = c.cfg.kv_dtype == SWA_DTYPE_E4M3;
+  P.scale_log2 = a.scale * 1.4426950408889634f * (f8 ? a.k_scale : 1.f);
+  P.v_scale = f8 ? a.v_scale : 1.f;
   P.out = static_cast<__nv_bfloat16 *>(a.out);
   P.desc = static_cast<MergeDesc *>(a.ws);
   P.partials = reinterpret_cast<float *>(static_cast<char *>(a.ws) + w.desc_bytes);
@@ -912,8 +1017,9 @@ cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree,
   CUtensorMap tmq;
   if (!make_q_tile_map(&tmq, a.q, a.nq, c.cfg.num_q_heads, c.cfg.head_dim, P.G, P.T))
     return cudaErrorInvalidValue;
-  return c.cfg.head_dim == 64 ? launch_tree<64>(L, tmq, P, w.rows, s)
-                              : launch_tree<128>(L, tmq, P, w.rows, s);
+  if (f8) return launch_tree<128, true>(L, tmq, P, w.rows, s);
+  return c.cfg.head_dim == 64 ? launch_tree<64, false>(L, tmq, P, w.rows, s)
+                              : launch_tree<128, false>(L, tmq, P, w.rows, s);
 }
 
 }  // namespace swa

@@ -385,10 +385,10 @@ def test_device_checks():
 
 
 @pytest.mark.parametrize("shape,ps,kernel", [(MIMO, 64, 3), (MIMO, 16, 3), (MIMO, 1, 0), (GPTOSS, 32, 3),
-                                             (TINY, 1, 0)],
-                         ids=["mimo-ps64", "mimo-ps16", "mimo-ps1", "gptoss", "tiny"])
+                                             (LLAMA4, 64, 3), (TINY, 1, 0)],
+                         ids=["mimo-ps64", "mimo-ps16", "mimo-ps1", "gptoss", "llama4", "tiny"])
 def test_kernel_taken(shape, ps, kernel):
-    """The tensor-core kernel serves bf16 pages of 16 to 64; -1 and 0 select."""
+    """The tensor-core kernel serves bf16 and E4M3 pages of 16 to 64; -1 and 0 select."""
     P, S = _step(shape, ps, [40], [[-1, 0, 0]])
     S.attend(1)
     assert api.swa_last_attn_path(P.ctx) == kernel
