@@ -865,9 +865,9 @@ swa_status swa_qk_norm_rope_store(swa_ctx *c, int32_t layer, const void *q, int6
     return p && ((reinterpret_cast<uintptr_t>(p) & 15) || (stride * esz) % 16 || stride < heads * d);
   };
   if (bad(q, q_stride, c->cfg.num_q_heads) || bad(k, k_stride, hkv) || bad(v, v_stride, hkv) ||
-      (reinterpret_cast<uintptr_t>(q_out) & 15))
+      ((reinterpret_cast<uintptr_t>(q_out) | reinterpret_cast<uintptr_t>(cos_sin)) & 15))
     return fail(c, SWA_ERR_INVALID,
-                "q, k, v and q_out need 16-byte aligned rows that do not overlap");
+                "q, k, v, q_out and cos_sin need 16-byte aligned rows that do not overlap");
   swa::QkNormArgs a{};
   a.q = q;
   a.k = k;

@@ -245,7 +245,7 @@ def test_refusals():
     for kw in (dict(layer=2), dict(layer=-1), dict(n=-1), dict(q=None), dict(out=None), dict(k=None), dict(v=None),
                dict(full=None), dict(q=None, out=None, k=None, v=None), dict(rot=-16), dict(rot=8), dict(rot=144),
                dict(pos=None), dict(table=None), dict(max_pos=0), dict(eps=-1.0), dict(eps=float("nan")),
-               dict(q=R.q.data_ptr() + 2), dict(k=R.k.data_ptr() + 8), dict(out=out.data_ptr() + 4),
+               dict(q=R.q.data_ptr() + 2), dict(k=R.k.data_ptr() + 8), dict(out=out.data_ptr() + 4), dict(table=table.data_ptr() + 4),
                dict(qs=st + 4), dict(vs=4 * 128 - 8), dict(ks=0)):
         assert call(**kw) == api.SWA_ERR_INVALID, kw
     assert call(n=0) == 0 and call() == 0 and call(rot=0, pos=None, table=None) == 0
