@@ -33,8 +33,9 @@
 namespace swa {
 namespace {
 
-constexpr int kNormWarps = 8;      // and a producer warp
-constexpr int kNormStages = 4;
+constexpr int kNormWarps = 4;      // and a producer warp
+constexpr int kNormCtas = 4;       // per SM
+constexpr int kNormStages = 2;
 constexpr int kStageRows = 24576;  // bytes of head rows of a stage
 constexpr int kStageTable = 512;   // bytes of an angle row (rot_dim <= 128)
 
@@ -59,6 +60,7 @@ struct NormParams {
   int64_t units;         // chunks of all tokens
   int chunks;            // chunks of a token
   int chunk_rows;        // rows of a chunk
+  int step_t, step_c;    // the grid as tokens and chunks
 };
 
 struct NormStage {
@@ -121,7 +123,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 // A unit is a chunk of one token's rows, counted through its query heads, key
 // heads and value heads (an absent input has none).
 template <typename T, int D, bool kF8, bool kInter>
-__global__ void __launch_bounds__((kNormWarps + 1) * 32, 2) k_qk_norm_rope_store(NormParams P) {
+__global__ void __launch_bounds__((kNormWarps + 1) * 32, kNormCtas) k_qk_norm_rope_store(NormParams P) {
   using Wd = Word<T>;
   constexpr int kEsz = (int)sizeof(T), kRow = D * kEsz;
   constexpr int W = Wd::kN, H = W / 2;    // values and pairs of a word
@@ -222,83 +224,112 @@ __global__ void __launch_bounds__((kNormWarps + 1) * 32, 2) k_qk_norm_rope_store
     const bool turned = li * 2 * W < P.rot; // rot is a multiple of 2 W
     const bool split = turned && !kInter;
     const int da = split ? li * W : li * 2 * W, db = split ? half + li * W : li * 2 * W + W;
-    int64_t k = 0;
-    for (int64_t u0 = blockIdx.x; u0 < P.units; u0 += step, ++k) {
-      const int s = (int)(k % kNormStages);
-      if (!__all_sync(0xffffffffu,
-                      tc::mbar_wait(full(s), (uint32_t)(k / kNormStages) & 1, &s_abort)))
-        break;
+    const int oa = da * kEsz, ob = db * kEsz;
+    float wq[2 * W], wk[2 * W];           // norm weights of the lane's values
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      wq[i] = P.qw ? P.qw[da + i] : 1.f;
+      wq[W + i] = P.qw ? P.qw[db + i] : 1.f;
+      wk[i] = P.kw ? P.kw[da + i] : 1.f;
+      wk[W + i] = P.kw ? P.kw[db + i] : 1.f;
+    }
+    int64_t t = blockIdx.x / P.chunks;
+    int c = (int)(blockIdx.x % P.chunks), s = 0;
+    uint32_t phase = 0;
+    for (int64_t u0 = blockIdx.x; u0 < P.units; u0 += step) {
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(full(s), phase, &s_abort))) break;
       const NormStage info = s_info[s];
-      const int64_t t = u0 / P.chunks;
-      const int r0 = (int)(u0 % P.chunks) * P.chunk_rows, r1 = min(r0 + P.chunk_rows, rows);
-      const char *tile = data(s);
-      const float *angles = reinterpret_cast<const float *>(tile + kStageRows);
-      // Rows of each kind in the chunk, in passes of RPW rows.
-      const int q1 = min(r1, nq), k0 = max(r0, nq), k1 = min(r1, nq + nk), v0 = max(r0, nq + nk);
-      const int pq = max(0, (q1 - r0 + RPW - 1) / RPW), pk = max(0, (k1 - k0 + RPW - 1) / RPW);
-      const int pv = max(0, (r1 - v0 + RPW - 1) / RPW);
-      const int total = info.ok ? pq + pk + pv : 0;
-      // Factors of a kind: out_a = x_a fa + z_a ga, out_b = x_b fb + z_b gb, z the
-      // pair's other values (halves: the other word; neighbours: swapped in place).
-      uint64_t fa[H], ga[H], fb[H], gb[H];
-      int have = -1;                      // kind whose factors are held
+      const int r0 = c * P.chunk_rows, r1 = info.ok ? min(r0 + P.chunk_rows, rows) : 0;
+      const char *tile = data(s) - r0 * kRow;           // row r at tile + r * kRow
+      // The token's angles at the lane's values (cosine 1, sine 0 where nothing turns).
+      float cs[2 * W], sn[2 * W];
+      if (turned) {
+        const float *ang = reinterpret_cast<const float *>(data(s) + kStageRows);
+        if (kInter) {
+#pragma unroll
+          for (int i = 0; i < 2 * W; i += 2) {
+            cs[i] = cs[i + 1] = ang[(da + i) >> 1];
+            sn[i + 1] = ang[half + ((da + i) >> 1)];
+            sn[i] = -sn[i + 1];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < W; i += 2) {
+            const float2 x = *reinterpret_cast<const float2 *>(ang + da + i);
+            const float2 y = *reinterpret_cast<const float2 *>(ang + half + da + i);
+            cs[i] = cs[W + i] = x.x;
+            cs[i + 1] = cs[W + i + 1] = x.y;
+            sn[W + i] = y.x;
+            sn[W + i + 1] = y.y;
+            sn[i] = -y.x;
+            sn[i + 1] = -y.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 * W; ++i) {
+          cs[i] = 1.f;
+          sn[i] = 0.f;
+        }
+      }
+      // Rows [lo, hi) of a kind, RPW per pass, the passes of all kinds dealt to
+      // the warps in turn: `pass` counts those before, this warp's first row
+      // follows.
+      int pass = 0;
+      auto first_row = [&](int lo, int hi) {
+        const int mine = lo + ((warp - pass) & (kNormWarps - 1)) * RPW;
+        if (hi > lo) pass += (hi - lo + RPW - 1) / RPW;
+        return mine;
+      };
+#pragma unroll 1
+      for (int kd = 0; kd < 2; ++kd) {    // query heads, key heads
+        const int lo = kd ? max(r0, nq) : r0, hi = min(r1, kd ? nq + nk : nq);
+        int rw = first_row(lo, hi);
+        if (rw >= hi) continue;
+        // Factors: out_a = x_a fa + z_a ga, out_b = x_b fb + z_b gb, z the pair's
+        // other values (halves: the other word; neighbours: swapped in place).
+        uint64_t fa[H], ga[H], fb[H], gb[H];
+        {
+          float f[2 * W], g[2 * W];
+#pragma unroll
+          for (int i = 0; i < 2 * W; ++i) {
+            const int other = kInter ? i ^ 1 : (i + W) % (2 * W);
+            f[i] = (kd ? wk[i] : wq[i]) * cs[i];
+            g[i] = (kd ? wk[other] : wq[other]) * sn[i];
+          }
+#pragma unroll
+          for (int i = 0; i < H; ++i) {
+            fa[i] = tc::f2pack(f[2 * i], f[2 * i + 1]);
+            fb[i] = tc::f2pack(f[W + 2 * i], f[W + 2 * i + 1]);
+            ga[i] = tc::f2pack(g[2 * i], g[2 * i + 1]);
+            gb[i] = tc::f2pack(g[W + 2 * i], g[W + 2 * i + 1]);
+          }
+        }
+        const bool norm = kd ? P.kw != nullptr : P.qw != nullptr;
+        const bool keep = kd == 0 || info.base >= 0;
+        char *out = kd ? P.addr.k + info.base - (int64_t)nq * (kF8 ? D : kRow)
+                       : P.q_out + t * P.hq * kRow;
+        const int out_row = kd && kF8 ? D : kRow;
 #pragma unroll 2
-      for (int p = warp; p < total; p += kNormWarps) {
-        const int kd = p < pq ? 0 : p < pq + pk ? 1 : 2;
-        const int r = (kd == 0 ? r0 + p * RPW : kd == 1 ? k0 + (p - pq) * RPW
-                                                        : v0 + (p - pq - pk) * RPW) + sub;
-        const bool live = r < (kd == 0 ? q1 : kd == 1 ? k1 : r1);
-        const char *src = tile + (live ? r - r0 : 0) * kRow;
-        const uint2 ra = *reinterpret_cast<const uint2 *>(src + da * kEsz);
-        const uint2 rb = *reinterpret_cast<const uint2 *>(src + db * kEsz);
-        uint64_t a[H], b[H];
-        Wd::get(ra, a);
-        Wd::get(rb, b);
-        if (kd != 2) {
-          const float *w = kd == 0 ? P.qw : P.kw;
-          if (have != kd) {
-            have = kd;
-            float xa[W], xb[W], ca[W], sa[W], cb[W], sb[W];
+        for (; rw < hi; rw += kNormWarps * RPW) {
+          const int r = rw + sub;
+          const bool live = r < hi && keep;
+          const char *src = tile + (r < hi ? r : rw) * kRow;
+          uint64_t a[H], b[H];
+          Wd::get(*reinterpret_cast<const uint2 *>(src + oa), a);
+          Wd::get(*reinterpret_cast<const uint2 *>(src + ob), b);
+          uint64_t s2 = mul2(a[0], a[0]);
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-              xa[i] = w ? w[da + i] : 1.f;
-              xb[i] = w ? w[db + i] : 1.f;
-              const int ia = kInter ? (da + i) >> 1 : da + i, ib = kInter ? (db + i) >> 1 : da + i;
-              ca[i] = turned ? angles[ia] : 1.f;
-              cb[i] = turned ? angles[ib] : 1.f;
-              sa[i] = turned ? angles[half + ia] : 0.f;
-              sb[i] = turned ? angles[half + ib] : 0.f;
-            }
-            float qa[W], qb[W];
+          for (int i = 1; i < H; ++i) s2 = tc::fma2(a[i], a[i], s2);
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-              const float za = kInter ? xa[i ^ 1] : xb[i], zb = kInter ? xb[i ^ 1] : xa[i];
-              qa[i] = (kInter && (i & 1)) ? za * sa[i] : -za * sa[i];
-              qb[i] = (kInter && !(i & 1)) ? -zb * sb[i] : zb * sb[i];
-            }
+          for (int i = 0; i < H; ++i) s2 = tc::fma2(b[i], b[i], s2);
+          float s0, s1;
+          tc::f2unpack(s2, s0, s1);
+          float ss = s0 + s1;
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-              fa[i] = tc::f2pack(xa[2 * i] * ca[2 * i], xa[2 * i + 1] * ca[2 * i + 1]);
-              fb[i] = tc::f2pack(xb[2 * i] * cb[2 * i], xb[2 * i + 1] * cb[2 * i + 1]);
-              ga[i] = tc::f2pack(qa[2 * i], qa[2 * i + 1]);
-              gb[i] = tc::f2pack(qb[2 * i], qb[2 * i + 1]);
-            }
-          }
-          uint64_t rs2 = tc::f2pack(1.f, 1.f);
-          if (w) {
-            uint64_t s2 = mul2(a[0], a[0]);
-#pragma unroll
-            for (int i = 1; i < H; ++i) s2 = tc::fma2(a[i], a[i], s2);
-#pragma unroll
-            for (int i = 0; i < H; ++i) s2 = tc::fma2(b[i], b[i], s2);
-            float s0, s1;
-            tc::f2unpack(s2, s0, s1);
-            float ss = s0 + s1;
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float rs = rsqrtf(ss * (1.f / D) + P.eps);
-            rs2 = tc::f2pack(rs, rs);
-          }
+          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float rs = norm ? rsqrtf(ss * (1.f / D) + P.eps) : 1.f;
+          const uint64_t rs2 = tc::f2pack(rs, rs);
           uint64_t ya[H], yb[H];
 #pragma unroll
           for (int i = 0; i < H; ++i) {
@@ -310,11 +341,11 @@ __global__ void __launch_bounds__((kNormWarps + 1) * 32, 2) k_qk_norm_rope_store
             for (int i = 0; i < H; ++i) {
               uint64_t za = b[i], zb = a[i];
               if (kInter) {
-                float lo, hi;
-                tc::f2unpack(a[i], lo, hi);
-                za = tc::f2pack(hi, lo);
-                tc::f2unpack(b[i], lo, hi);
-                zb = tc::f2pack(hi, lo);
+                float x, y;
+                tc::f2unpack(a[i], x, y);
+                za = tc::f2pack(y, x);
+                tc::f2unpack(b[i], x, y);
+                zb = tc::f2pack(y, x);
               }
               ya[i] = tc::fma2(za, ga[i], ya[i]);
               yb[i] = tc::fma2(zb, gb[i], yb[i]);
@@ -322,31 +353,58 @@ __global__ void __launch_bounds__((kNormWarps + 1) * 32, 2) k_qk_norm_rope_store
           }
 #pragma unroll
           for (int i = 0; i < H; ++i) {
-            a[i] = mul2(ya[i], rs2);
-            b[i] = mul2(yb[i], rs2);
+            ya[i] = mul2(ya[i], rs2);
+            yb[i] = mul2(yb[i], rs2);
+          }
+          if (live) {
+            char *dst = out + r * out_row;
+            if (kF8 && kd) {
+              if constexpr (kF8) {
+                *reinterpret_cast<uint32_t *>(dst + da) = encode4(ya, P.k_scale);
+                *reinterpret_cast<uint32_t *>(dst + db) = encode4(yb, P.k_scale);
+              }
+            } else {
+              *reinterpret_cast<uint2 *>(dst + oa) = Wd::put(ya);
+              *reinterpret_cast<uint2 *>(dst + ob) = Wd::put(yb);
+            }
           }
         }
-        if (kd == 0) {
-          if (live) {
-            char *dst = P.q_out + (t * P.hq + r) * kRow;
-            *reinterpret_cast<uint2 *>(dst + da * kEsz) = Wd::put(a);
-            *reinterpret_cast<uint2 *>(dst + db * kEsz) = Wd::put(b);
-          }
-        } else if (live && info.base >= 0) {
-          const int h = r - nq - (kd == 2 ? nk : 0);
-          char *dst = (kd == 2 ? P.addr.v : P.addr.k) + info.base;
+      }
+      {                                   // value heads: stored as they are
+        const int lo = max(r0, nq + nk), hi = info.base >= 0 ? r1 : 0;
+        for (int rw = first_row(lo, hi); rw < hi; rw += kNormWarps * RPW) {
+          const int r = rw + sub;
+          if (r >= hi) continue;
+          const char *src = tile + r * kRow;
+          const uint2 ra = *reinterpret_cast<const uint2 *>(src + oa);
+          const uint2 rb = *reinterpret_cast<const uint2 *>(src + ob);
+          char *dst = P.addr.v + info.base;
           if constexpr (kF8) {
-            const float sc = kd == 2 ? P.v_scale : P.k_scale;
-            *reinterpret_cast<uint32_t *>(dst + h * D + da) = encode4(a, sc);
-            *reinterpret_cast<uint32_t *>(dst + h * D + db) = encode4(b, sc);
+            dst += (r - nq - nk) * D;
+            uint64_t a[H], b[H];
+            Wd::get(ra, a);
+            Wd::get(rb, b);
+            *reinterpret_cast<uint32_t *>(dst + da) = encode4(a, P.v_scale);
+            *reinterpret_cast<uint32_t *>(dst + db) = encode4(b, P.v_scale);
           } else {
-            *reinterpret_cast<uint2 *>(dst + h * kRow + da * kEsz) = kd == 2 ? ra : Wd::put(a);
-            *reinterpret_cast<uint2 *>(dst + h * kRow + db * kEsz) = kd == 2 ? rb : Wd::put(b);
+            dst += (r - nq - nk) * kRow;
+            *reinterpret_cast<uint2 *>(dst + oa) = ra;
+            *reinterpret_cast<uint2 *>(dst + ob) = rb;
           }
         }
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(empty(s));
+      if (++s == kNormStages) {
+        s = 0;
+        phase ^= 1;
+      }
+      t += P.step_t;
+      c += P.step_c;
+      if (c >= P.chunks) {
+        c -= P.chunks;
+        ++t;
+      }
     }
   }
   __syncthreads();
@@ -364,7 +422,7 @@ template <typename T, int D, bool kF8, bool kInter>
 cudaError_t launch_one(const Ctx &c, NormParams P, int64_t n, cudaStream_t s) {
   constexpr int kRow = D * (int)sizeof(T), kSmem = kNormStages * (kStageRows + kStageTable);
   const int rows = (P.q ? P.hq : 0) + (P.k ? 2 * P.hkv : 0);
-  const int64_t ctas = 2LL * (c.num_sms > 0 ? c.num_sms : 148);
+  const int64_t ctas = (int64_t)kNormCtas * (c.num_sms > 0 ? c.num_sms : 148);
   // A chunk is a whole token where that fits a stage and there are tokens for
   // all CTAs; fewer tokens are cut finer, down to 16 rows.
   const int64_t even = (n * rows + ctas - 1) / ctas;
@@ -376,6 +434,8 @@ cudaError_t launch_one(const Ctx &c, NormParams P, int64_t n, cudaStream_t s) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int64_t grid = P.units < ctas ? P.units : ctas;
+  P.step_t = (int)(grid / P.chunks);
+  P.step_c = (int)(grid % P.chunks);
   k_qk_norm_rope_store<T, D, kF8, kInter><<<(unsigned)grid, (kNormWarps + 1) * 32, kSmem, s>>>(P);
   return cudaGetLastError();
 }
