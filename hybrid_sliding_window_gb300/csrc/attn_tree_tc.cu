@@ -282,7 +282,9 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  // All 512 columns: the allocation starts at address 0, which the addresses
+  // below then hold as constants.
+  constexpr uint32_t tmem = 0;
   constexpr uint32_t kIdS = idesc_f16(128, 128, false, kF8);
   constexpr uint32_t kIdO = idesc_f16(128, kD, true, kF8);
 
@@ -527,16 +529,13 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     // ===================== MMA issue =====================
     // Step u of a segment belongs to softmax group u & 1 and key tile u / 2 (two
     // Q tiles) or u; the order is S(0), S(1), then per step O(u), S(u + 2).  The
-    // whole warp runs the loop and one lane executes the tensor-core
-    // instructions, so that the descriptors are computed in uniform registers
-    // (values that came from shared memory are made uniform by a shuffle); in a
-    // branch of that lane alone each product cost about 100 cycles to issue.
-    auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-    const bool lead = lane == 0;
-    const uint32_t tm = uni((int)tmem), sbu = uni((int)sb);
-    const uint64_t dq = smem_desc(sbu, 16, 1024);
-    const uint64_t dk = smem_desc(sbu + Gm::kOffRing, 16, 1024);
-    const uint64_t dv = smem_desc(sbu + Gm::kOffRing, kBlock, 1024);
+    // whole warp runs the loop and an elected lane executes the tensor-core
+    // instructions: with the segment's numbers made uniform by a warp reduction,
+    // descriptors are computed in uniform registers.
+    auto uni = [](int x) { return (int)__reduce_max_sync(0xffffffffu, x); };
+    const uint64_t dq = smem_desc(sb, 16, 1024);
+    const uint64_t dk = smem_desc(sb + Gm::kOffRing, 16, 1024);
+    const uint64_t dv = smem_desc(sb + Gm::kOffRing, kBlock, 1024);
     int steps0 = 0, steps1 = 0;              // steps of each group so far
     int base = 0;                            // ring position of the segment's first tile
     for (int nd = 0;; ++nd) {
@@ -544,31 +543,15 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       if (!wait_all(bar(B_IFULL + slot), (nd >> 1) & 1)) break;
       const int n = uni(s_seg[slot].n_tiles), two = uni(s_seg[slot].two), b = uni(s_seg[slot].b);
       __syncwarp();
-      if (lead) mbar_arrive(bar(B_IEMPTY + slot));
+      if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
       if (b < 0) break;
       const int U = two ? 2 * n : n;
       if (!wait_all(bar(kF8 ? B_QCONV : B_FULLQ), nd & 1)) break;
-      auto issue_s = [&](int u) {
-        const int g = u & 1, r = base + seq_k(two ? u >> 1 : u);
-        const int s = r % kStages;
-        if (!wait_all(bar(B_FULL + s), (r / kStages) & 1)) return false;
-        tc_fence_after();
-        const uint64_t kd = dk + (uint64_t)(s * kTileBytes >> 4);
-        const uint64_t qd = dq + (uint64_t)((two && g ? kTileBytes : 0) >> 4);
-#pragma unroll
-        for (int ks = 0; ks < kD / 16; ++ks) {
-          const uint64_t off = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
-          mma_ss_lead(lead, tm + g * 128, qd + off, kd + off, kIdS, ks > 0);
-        }
-        tc_commit_lead(lead, bar(B_SDONE + g));
-        if (!two || g) tc_commit_lead(lead, bar(B_EMPTY + s));
-        if (u == U - 1) tc_commit_lead(lead, bar(B_QFREE));
-        return true;
-      };
       bool ok = true;
       for (int u = -2; u < U && ok; ++u) {   // u = -2, -1: S(0) and S(1) only
+        const int g = u & 1;
         if (u >= 0) {
-          const int g = u & 1, t = two ? u >> 1 : u;
+          const int t = two ? u >> 1 : u;
           const int r = base + seq_v(t, n), s = r % kStages;
           if (!(ok = wait_all(bar(B_FULL + s), (r / kStages) & 1))) break;
           if (!(ok = wait_all(bar(B_PREADY + g), (g ? steps1 : steps0) & 1))) break;
@@ -576,17 +559,37 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
           else ++steps0;
           tc_fence_after();
           const uint64_t vd = dv + (uint64_t)(s * kTileBytes >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < kKeys / 16; ++ks)
-            mma_ts_lead(lead, tm + 256 + g * kD, tm + g * 128 + ks * 8,
-                        vd + (uint64_t)(ks * 16 * 128 >> 4), kIdO, (u >= 2 || ks > 0) ? 1u : 0u);
-          if (!two || g) tc_commit_lead(lead, bar(B_EMPTY + s));
-          if (u + 2 >= U) tc_commit_lead(lead, bar(B_ODONE + g));
+            for (int ks = 0; ks < kKeys / 16; ++ks)
+              mma_ts(tmem + 256 + g * kD, tmem + g * 128 + ks * 8,
+                     vd + (uint64_t)(ks * 16 * 128 >> 4), kIdO, (u >= 2 || ks > 0) ? 1u : 0u);
+            if (!two || g) tc_commit(bar(B_EMPTY + s));
+            if (u + 2 >= U) tc_commit(bar(B_ODONE + g));
+            if (U == 1) tc_commit(bar(B_ODONE + 1));
+          }
+          __syncwarp();
         }
-        if (u + 2 < U) ok = issue_s(u + 2);
+        if (u + 2 < U) {                     // S(u + 2), of the same group
+          const int r = base + seq_k(two ? (u + 2) >> 1 : u + 2), s = r % kStages;
+          if (!(ok = wait_all(bar(B_FULL + s), (r / kStages) & 1))) break;
+          tc_fence_after();
+          const uint64_t kd = dk + (uint64_t)(s * kTileBytes >> 4);
+          const uint64_t qd = dq + (uint64_t)((two && g ? kTileBytes : 0) >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < kD / 16; ++ks) {
+              const uint64_t off = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
+              mma_ss(tmem + g * 128, qd + off, kd + off, kIdS, ks > 0);
+            }
+            tc_commit(bar(B_SDONE + g));
+            if (!two || g) tc_commit(bar(B_EMPTY + s));
+            if (u + 3 == U) tc_commit(bar(B_QFREE));
+          }
+          __syncwarp();
+        }
       }
       if (!ok) break;
-      if (U == 1) tc_commit_lead(lead, bar(B_ODONE + 1));
       base += 2 * n;
     }
   } else if (warp < 8) {
@@ -854,7 +857,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
         if (fills) mbar_drain(bar(bLoadFull + s), (fills - 1) & 1);
       }
     if (warp == 10 && lane == 0 && q_issued) mbar_drain(bar(B_FULLQ), (q_issued - 1) & 1);
-    if (warp == 8 && lane == 0) {
+    if (warp == 8 && elect_one()) {
       tc_commit(bar(B_DRAIN));
       mbar_drain(bar(B_DRAIN), 0);
     }

@@ -134,31 +134,15 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, 
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
 }
-// The same two products and the commit, executed by the lanes whose `lead` is
-// set (one of a warp) in code that the whole warp runs: descriptors that are
-// uniform over the warp then stay in uniform registers, where the instruction
-// wants them.
-__device__ __forceinline__ void mma_ss_lead(bool lead, uint32_t d, uint64_t a, uint64_t b,
-                                            uint32_t idesc, uint32_t acc) {
+// One lane of the (converged) warp, the same one every time.  In the branch of
+// the elected lane, code keeps warp-uniform values in uniform registers, where
+// the tensor-core instructions want their descriptors.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"((uint32_t)lead));
-}
-__device__ __forceinline__ void mma_ts_lead(bool lead, uint32_t d, uint32_t a_tmem, uint64_t b,
-                                            uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"((uint32_t)lead));
-}
-__device__ __forceinline__ void tc_commit_lead(bool lead, uint32_t bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-          bar),
-      "r"((uint32_t)lead)
-      : "memory");
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile(
