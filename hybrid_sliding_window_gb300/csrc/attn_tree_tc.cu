@@ -126,7 +126,6 @@ struct Segment {
 // start is 1024-byte aligned: the tiles leave no room for an alignment gap.)
 struct Control {
   Segment seg[2];
-  int32_t rows[2][32];       // page rows of 32 page slots, double-buffered
   uint32_t tmem;
   int abort;
 };
@@ -234,7 +233,6 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
   Control *ctl = reinterpret_cast<Control *>(smem + Gm::kOffCtl);
   volatile int &s_abort = ctl->abort;
   Segment *s_seg = ctl->seg;
-  auto &s_rows = ctl->rows;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int kvh = blockIdx.x % P.hkv, group_id = blockIdx.x / P.hkv;
@@ -343,40 +341,42 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
         const int64_t col = max((pg0 + i) << P.ps_shift, lo);
         return page_rec(full_layer, P.ps_shift, rt_row, hdr, pages, col);
       };
-      s_rows[0][lane] = page_row(P, full_layer, rec_of(0));
+      int32_t rows = page_row(P, full_layer, rec_of(0));   // of batch `cur`, lane i: slot i
+      int32_t rows_old = rows;                             // of the batch before
       int32_t rec_next = n_slots > 32 ? rec_of(1) : 0;
-      __syncwarp();
-      int cur = 0;                           // batch of 32 slots held in s_rows[cur & 1]
+      int cur = 0;
       // Tiles in ring order: K0, then per tile the next K and this V.
       for (int j = 0; j < 2 * sg.n_tiles && ok; ++j) {
         const bool is_v = j == 2 * sg.n_tiles - 1 || (j > 0 && (j & 1) == 0);
         const int t = is_v ? (j == 2 * sg.n_tiles - 1 ? sg.n_tiles - 1 : j / 2 - 1) : (j + 1) / 2;
         const int i0 = t * ppt;
-        // K runs one tile ahead of V, so a batch's table stays until its last
-        // V is issued: two tables, the next one filled when K enters it.
+        // K runs one tile ahead of V, so the batch before stays at hand.
         if (!is_v && (i0 >> 5) > cur) {
-          cur = i0 >> 5;
-          s_rows[cur & 1][lane] = page_row(P, full_layer, rec_next);
+          ++cur;
+          rows_old = rows;
+          rows = page_row(P, full_layer, rec_next);
           rec_next = 32 * (cur + 1) < n_slots ? rec_of(cur + 1) : 0;
-          __syncwarp();
         }
-        int good = 1;
-        if (lane == 0) {
-          const int s = ring_issued % kLoads, f = ring_issued / kLoads;
-          if (f >= 1) good = mbar_wait(bar(bLoadEmpty + s), (f - 1) & 1, &s_abort);
-          if (good) {
-            const int32_t *rows = &s_rows[(i0 >> 5) & 1][i0 & 31];
-            const uint32_t dst = sb + kOffLoad + s * kLoadBytes, full = bar(bLoadFull + s);
-            mbar_expect_tx(full, (uint32_t)kLoadBytes);
-            for (int i = 0; i < ppt; ++i)
+        const int32_t mine_rows = (i0 >> 5) == cur ? rows : rows_old;
+        int32_t row[8];                      // first rows of the tile's pages
+#pragma unroll
+        for (int i = 0; i < 8; ++i) row[i] = __shfl_sync(0xffffffffu, mine_rows, (i0 + i) & 31);
+        const int s = ring_issued % kLoads, f = ring_issued / kLoads;
+        if (f >= 1 && !(ok = wait_all(bar(bLoadEmpty + s), (f - 1) & 1))) break;
+        const uint32_t dst = sb + kOffLoad + s * kLoadBytes, full = bar(bLoadFull + s);
+        const CUtensorMap *map = is_v ? &tmV : &tmK;
+        if (elect_one()) {
+          mbar_expect_tx(full, (uint32_t)kLoadBytes);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < ppt)
+#pragma unroll
               for (int h = 0; h < (kF8 ? 1 : kD / 64); ++h)
-                tma_load_3d(dst + h * kBlock + (i << P.ps_shift) * 128, is_v ? &tmV : &tmK, h * 64,
-                            kvh, rows[i], full);
-            ++ring_issued;
-          }
+                tma_load_3d(dst + h * kBlock + (i << P.ps_shift) * 128, map, h * 64, kvh, row[i],
+                            full);
         }
-        ok = __shfl_sync(0xffffffffu, good, 0) != 0;
         __syncwarp();
+        ++ring_issued;
       }
     };
 
