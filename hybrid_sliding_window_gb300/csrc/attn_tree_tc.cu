@@ -528,10 +528,11 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
   } else if (warp == 8) {
     // ===================== MMA issue =====================
     // Step u of a segment belongs to softmax group u & 1 and key tile u / 2 (two
-    // Q tiles) or u; the order is S(0), S(1), then per step O(u), S(u + 2).  The
-    // whole warp runs the loop and an elected lane executes the tensor-core
-    // instructions: with the segment's numbers made uniform by a warp reduction,
-    // descriptors are computed in uniform registers.
+    // Q tiles) or u; the order is S(0), S(1), then per step O(u), S(u + 2).  An
+    // elected lane runs a segment's steps: with the segment's numbers made
+    // uniform by a warp reduction, descriptors are computed in uniform registers
+    // (in a branch on the lane number a product cost 67 cycles to issue, whatever
+    // its size).
     auto uni = [](int x) { return (int)__reduce_max_sync(0xffffffffu, x); };
     const uint64_t dq = smem_desc(sb, 16, 1024);
     const uint64_t dk = smem_desc(sb + Gm::kOffRing, 16, 1024);
@@ -547,19 +548,18 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       if (b < 0) break;
       const int U = two ? 2 * n : n;
       if (!wait_all(bar(kF8 ? B_QCONV : B_FULLQ), nd & 1)) break;
-      bool ok = true;
-      for (int u = -2; u < U && ok; ++u) {   // u = -2, -1: S(0) and S(1) only
-        const int g = u & 1;
-        if (u >= 0) {
-          const int t = two ? u >> 1 : u;
-          const int r = base + seq_v(t, n), s = r % kStages;
-          if (!(ok = wait_all(bar(B_FULL + s), (r / kStages) & 1))) break;
-          if (!(ok = wait_all(bar(B_PREADY + g), (g ? steps1 : steps0) & 1))) break;
-          if (g) ++steps1;
-          else ++steps0;
-          tc_fence_after();
-          const uint64_t vd = dv + (uint64_t)(s * kTileBytes >> 4);
-          if (elect_one()) {
+      int ok = 1;
+      if (elect_one()) {
+        for (int u = -2; u < U; ++u) {       // u = -2, -1: S(0) and S(1) only
+          const int g = u & 1;
+          if (u >= 0) {
+            const int t = two ? u >> 1 : u;
+            const int r = base + seq_v(t, n), s = r % kStages;
+            if (!(ok = mbar_wait(bar(B_FULL + s), (r / kStages) & 1, &s_abort))) break;
+            if (!(ok = mbar_wait(bar(B_PREADY + g), ((g ? steps1 : steps0) + (u >> 1)) & 1, &s_abort)))
+              break;
+            tc_fence_after();
+            const uint64_t vd = dv + (uint64_t)(s * kTileBytes >> 4);
 #pragma unroll
             for (int ks = 0; ks < kKeys / 16; ++ks)
               mma_ts(tmem + 256 + g * kD, tmem + g * 128 + ks * 8,
@@ -568,15 +568,12 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
             if (u + 2 >= U) tc_commit(bar(B_ODONE + g));
             if (U == 1) tc_commit(bar(B_ODONE + 1));
           }
-          __syncwarp();
-        }
-        if (u + 2 < U) {                     // S(u + 2), of the same group
-          const int r = base + seq_k(two ? (u + 2) >> 1 : u + 2), s = r % kStages;
-          if (!(ok = wait_all(bar(B_FULL + s), (r / kStages) & 1))) break;
-          tc_fence_after();
-          const uint64_t kd = dk + (uint64_t)(s * kTileBytes >> 4);
-          const uint64_t qd = dq + (uint64_t)((two && g ? kTileBytes : 0) >> 4);
-          if (elect_one()) {
+          if (u + 2 < U) {                   // S(u + 2), of the same group
+            const int r = base + seq_k(two ? (u + 2) >> 1 : u + 2), s = r % kStages;
+            if (!(ok = mbar_wait(bar(B_FULL + s), (r / kStages) & 1, &s_abort))) break;
+            tc_fence_after();
+            const uint64_t kd = dk + (uint64_t)(s * kTileBytes >> 4);
+            const uint64_t qd = dq + (uint64_t)((two && g ? kTileBytes : 0) >> 4);
 #pragma unroll
             for (int ks = 0; ks < kD / 16; ++ks) {
               const uint64_t off = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
@@ -586,10 +583,11 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
             if (!two || g) tc_commit(bar(B_EMPTY + s));
             if (u + 3 == U) tc_commit(bar(B_QFREE));
           }
-          __syncwarp();
         }
       }
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, ok)) break;
+      steps0 += (U + 1) >> 1;
+      steps1 += U >> 1;
       base += 2 * n;
     }
   } else if (warp < 8) {
