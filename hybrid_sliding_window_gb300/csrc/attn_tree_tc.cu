@@ -27,10 +27,13 @@
 // phases following running counts so that nothing drains between segments:
 //   * warp 9, the producer, finds the CTA's segments (warp-wide prefix sums over
 //     the requests), hands them to the other roles through a two-slot ring,
-//     looks page rows up 32 page slots at a time and streams K and V tiles by
-//     TMA through one ring, in the order in which the MMAs use them;
+//     looks page rows up 32 page slots at a time and loads K tiles by TMA; warp
+//     11 does the same for V.  K and V tiles share one ring, in the order in
+//     which the products use them.  (One warp for both: a TMA box costs its
+//     issuing thread 75 to 100 cycles, sixteen of them per tile pair on pages
+//     of 16 rows, which was the pace of such layers.)
 //   * warp 10 loads each segment's Q tiles once the previous segment's last
-//     QK^T has read them (E4M3 KV: and converts, below);
+//     QK^T has read them;
 //   * warp 8 issues S = Q K^T and O += P V with P in TMEM over S;
 //   * warps 0-3 and 4-7 are two softmax groups.  Rows of an item that fill two
 //     Q tiles: one tile each, both read the same key tiles.  Rows that fit one
@@ -66,7 +69,7 @@ using namespace tc;
 constexpr int kTileRows = 128;               // rows of a Q tile (M)
 constexpr int kKeys = 128;                   // keys of a K/V tile
 constexpr int kBlock = kTileRows * 64 * 2;   // one 64-column block of a tile
-constexpr int kTreeThreads = 352;            // 8 softmax warps, MMA, producer, Q loader
+constexpr int kTreeThreads = 384;            // 8 softmax warps, MMA, and three that load
 constexpr int kConvThreads = 64;             // E4M3 KV: warps 10 and 11 convert
 constexpr float kRescaleGap = 8.f;           // log2 units: rescale O when the max grows more
 constexpr float kSumCap = 32768.f;           // a chunk's weight sum that forces a maximum pass
@@ -84,7 +87,6 @@ struct TreeGeo {
   static constexpr int kOffStat = kOffRaw + kRawStages * kRawBytes;
   static constexpr int kOffBars = kOffStat + 2 * kTileRows * 8;
   static constexpr int kOffCtl = kOffBars + 40 * 8;           // Control
-  static constexpr int kThreads = F8 ? 384 : kTreeThreads;
 };
 
 struct TreeParams {
@@ -126,6 +128,7 @@ struct Segment {
 // start is 1024-byte aligned: the tiles leave no room for an alignment gap.)
 struct Control {
   Segment seg[2];
+  int fills[8];              // fills of each slot of the loads' ring
   uint32_t tmem;
   int abort;
 };
@@ -214,7 +217,7 @@ __device__ __forceinline__ int tile_off(int r, int c) {
 }
 
 template <int kD, bool kF8>
-__global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
+__global__ void __launch_bounds__(kTreeThreads, 1)
     k_tree_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
               const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TreeParams P) {
   using Gm = TreeGeo<kD, kF8>;
@@ -247,6 +250,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     return;
   }
   if (tid == 0) s_abort = 0;
+  if (tid < 8) ctl->fills[tid] = 0;
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
                      smem_u32(&ctl->tmem)),
@@ -256,8 +260,8 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_IFULL + i), 1);
-      // 8 softmax warps, the MMA lane, the Q loader (or two converters)
-      mbar_init(bar(B_IEMPTY + i), kF8 ? 11 : 10);
+      // 8 softmax warps, the MMA warp, and Q and V loaders or two converters
+      mbar_init(bar(B_IEMPTY + i), 11);
       mbar_init(bar(B_SDONE + i), 1);
       mbar_init(bar(B_PREADY + i), kTileRows);
       mbar_init(bar(B_ODONE + i), 1);
@@ -286,8 +290,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
   constexpr uint32_t kIdS = idesc_f16(128, 128, false, kF8);
   constexpr uint32_t kIdO = idesc_f16(128, kD, true, kF8);
 
-  // Loads issued, for the abort path: ring slots filled (producer), Q fills.
-  int ring_issued = 0, q_issued = 0;
+  int q_issued = 0;                          // Q fills, for the abort path
 
   // Warp-collective, warp 10: the Q tiles of the CTA's segment nd, once the last
   // QK^T of the one before has read the buffers.
@@ -306,11 +309,78 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     return true;
   };
 
+  // Warp-collective: the K tiles, the V tiles or both (kinds 1, 2, 3) of a
+  // segment whose first tile has position `base` in the ring of the loads.
+  const bool full_layer = P.kind == SWA_LAYER_FULL;
+  const int ppt = kKeys >> P.ps_shift;       // pages per key tile
+  auto stream = [&](const Segment &sg, int base, int kinds) {
+    const int32_t *rt_row = full_layer ? P.rt + P.req_idx[sg.b] * P.rt_stride : nullptr;
+    const int32_t *hdr = full_layer ? nullptr : P.plan.hdr + sg.b * 4;
+    const int32_t *pages = full_layer ? nullptr : P.plan.pages + (int64_t)sg.b * P.plan.max_pages;
+    const int64_t pg0 = sg.col0 >> P.ps_shift;
+    const int64_t hi = sg.prefix + sg.n0 + sg.n_tok - 1;   // the item's last column
+    // A windowed request's first page may start before its first planned
+    // column: look it up by a column that is in the plan.
+    const int64_t lo = full_layer ? 0 : first_position(P.kind, P.window, sg.prefix);
+    const int n_pg = (int)((hi >> P.ps_shift) - pg0 + 1);
+    const int n = sg.n_tiles, n_slots = n * ppt;
+    // Page slots behind the last column load its page again: finite values,
+    // zero weight.
+    auto rec_of = [&](int k) {
+      const int i = min(32 * k + lane, n_pg - 1);
+      const int64_t col = max((pg0 + i) << P.ps_shift, lo);
+      return page_rec(full_layer, P.ps_shift, rt_row, hdr, pages, col);
+    };
+    int32_t rows = page_row(P, full_layer, rec_of(0));   // of batch `cur`, lane i: slot i
+    int32_t rows_old = rows;                             // of the batch before
+    int32_t rec_next = n_slots > 32 ? rec_of(1) : 0;
+    int cur = 0;
+    auto load_tile = [&](int t, int pos, const CUtensorMap *map) {
+      const int i0 = t * ppt;
+      if ((i0 >> 5) > cur) {
+        ++cur;
+        rows_old = rows;
+        rows = page_row(P, full_layer, rec_next);
+        rec_next = 32 * (cur + 1) < n_slots ? rec_of(cur + 1) : 0;
+      }
+      const int32_t held = (i0 >> 5) == cur ? rows : rows_old;
+      int32_t row[8];                        // first rows of the tile's pages
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < ppt) row[i] = __shfl_sync(0xffffffffu, held, (i0 + i) & 31);
+      // The slot's fill before this one may be the other warp's.  Its phase is
+      // told by parity alone, which is enough: this warp's previous tile lies at
+      // most three places back and its wait saw a place released that only the
+      // next place's release can precede, so the fill before that one is gone.
+      const int s = pos % kLoads, f = pos / kLoads;
+      if (f >= 1 && !wait_all(bar(bLoadEmpty + s), (f - 1) & 1)) return false;
+      const uint32_t dst = sb + kOffLoad + s * kLoadBytes, full = bar(bLoadFull + s);
+      if (elect_one()) {
+        mbar_expect_tx(full, (uint32_t)kLoadBytes);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < ppt)
+#pragma unroll
+            for (int h = 0; h < (kF8 ? 1 : kD / 64); ++h)
+              tma_load_3d(dst + h * kBlock + (i << P.ps_shift) * 128, map, h * 64, kvh, row[i],
+                          full);
+        ctl->fills[s] = f + 1;
+      }
+      __syncwarp();
+      return true;
+    };
+    // In ring order; K runs one tile ahead of V.
+    for (int t = 0; t <= n; ++t) {
+      if ((kinds & 1) && t < n && !load_tile(t, base + seq_k(t), &tmK)) return false;
+      if ((kinds & 2) && t > 0 && !load_tile(t - 1, base + seq_v(t - 1, n), &tmV)) return false;
+    }
+    return true;
+  };
+
   if (warp == 9) {
-    // ===================== producer: segments, K/V tiles =====================
-    const bool full_layer = P.kind == SWA_LAYER_FULL;
-    const int ppt = kKeys >> P.ps_shift;     // pages per key tile
-    int n_pub = 0;
+    // ===================== producer: segments, K tiles (E4M3 KV: and V) =====================
+    int n_pub = 0, base = 0;                 // segments published; ring position
+
     bool ok = true;
     MergeDesc mine{0, 0, 0};
     auto publish = [&](const Segment &sg) {
@@ -324,62 +394,6 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       ++n_pub;
       return true;
     };
-    auto stream = [&](const Segment &sg, int64_t hi) {   // hi: the item's last column
-      const int32_t *rt_row = full_layer ? P.rt + P.req_idx[sg.b] * P.rt_stride : nullptr;
-      const int32_t *hdr = full_layer ? nullptr : P.plan.hdr + sg.b * 4;
-      const int32_t *pages = full_layer ? nullptr : P.plan.pages + (int64_t)sg.b * P.plan.max_pages;
-      const int64_t pg0 = sg.col0 >> P.ps_shift;
-      // A windowed request's first page may start before its first planned
-      // column: look it up by a column that is in the plan.
-      const int64_t lo = full_layer ? 0 : first_position(P.kind, P.window, sg.prefix);
-      const int n_pg = (int)((hi >> P.ps_shift) - pg0 + 1);
-      const int n_slots = sg.n_tiles * ppt;
-      // Page slots behind the last column load its page again: finite values,
-      // zero weight.
-      auto rec_of = [&](int k) {
-        const int i = min(32 * k + lane, n_pg - 1);
-        const int64_t col = max((pg0 + i) << P.ps_shift, lo);
-        return page_rec(full_layer, P.ps_shift, rt_row, hdr, pages, col);
-      };
-      int32_t rows = page_row(P, full_layer, rec_of(0));   // of batch `cur`, lane i: slot i
-      int32_t rows_old = rows;                             // of the batch before
-      int32_t rec_next = n_slots > 32 ? rec_of(1) : 0;
-      int cur = 0;
-      // Tiles in ring order: K0, then per tile the next K and this V.
-      for (int j = 0; j < 2 * sg.n_tiles && ok; ++j) {
-        const bool is_v = j == 2 * sg.n_tiles - 1 || (j > 0 && (j & 1) == 0);
-        const int t = is_v ? (j == 2 * sg.n_tiles - 1 ? sg.n_tiles - 1 : j / 2 - 1) : (j + 1) / 2;
-        const int i0 = t * ppt;
-        // K runs one tile ahead of V, so the batch before stays at hand.
-        if (!is_v && (i0 >> 5) > cur) {
-          ++cur;
-          rows_old = rows;
-          rows = page_row(P, full_layer, rec_next);
-          rec_next = 32 * (cur + 1) < n_slots ? rec_of(cur + 1) : 0;
-        }
-        const int32_t mine_rows = (i0 >> 5) == cur ? rows : rows_old;
-        int32_t row[8];                      // first rows of the tile's pages
-#pragma unroll
-        for (int i = 0; i < 8; ++i) row[i] = __shfl_sync(0xffffffffu, mine_rows, (i0 + i) & 31);
-        const int s = ring_issued % kLoads, f = ring_issued / kLoads;
-        if (f >= 1 && !(ok = wait_all(bar(bLoadEmpty + s), (f - 1) & 1))) break;
-        const uint32_t dst = sb + kOffLoad + s * kLoadBytes, full = bar(bLoadFull + s);
-        const CUtensorMap *map = is_v ? &tmV : &tmK;
-        if (elect_one()) {
-          mbar_expect_tx(full, (uint32_t)kLoadBytes);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i < ppt)
-#pragma unroll
-              for (int h = 0; h < (kF8 ? 1 : kD / 64); ++h)
-                tma_load_3d(dst + h * kBlock + (i << P.ps_shift) * 128, map, h * 64, kvh, row[i],
-                            full);
-        }
-        __syncwarp();
-        ++ring_issued;
-      }
-    };
-
     // The head's line of tiles (or items), and this CTA's stretch of it.
     int64_t total = 0;
     for (int b0 = 0; b0 < P.bs; b0 += 32) total += request(P, b0 + lane).tiles;
@@ -436,8 +450,8 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
                 sg.part = 0;
               }
             }
-            ok = publish(sg);
-            if (ok) stream(sg, hi);
+            ok = publish(sg) && stream(sg, base, kF8 ? 3 : 1);
+            base += 2 * sg.n_tiles;
           }
           s = e;
         }
@@ -452,14 +466,16 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     }
   } else if (warp >= 10) {
     if constexpr (!kF8) {
-      // ===================== Q tiles =====================
+      // ===================== Q tiles (warp 10), V tiles (warp 11) =====================
+      int base = 0;
       for (int nd = 0;; ++nd) {
         const int slot = nd & 1;
         if (!wait_all(bar(B_IFULL + slot), (nd >> 1) & 1)) break;
         const Segment sg = s_seg[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
-        if (sg.b < 0 || !load_q(sg, nd)) break;
+        if (sg.b < 0 || !(warp == 10 ? load_q(sg, nd) : stream(sg, base, 2))) break;
+        base += 2 * sg.n_tiles;
       }
     } else {
       // ============ converters (E4M3 KV): Q, K and V to f16 ============
@@ -850,10 +866,8 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     // before the shared memory and TMEM they write are released.
     if (tid == 0) set_error(P.err, SWA_DEVERR_TIMEOUT);
     if (warp == 9 && lane == 0)
-      for (int s = 0; s < kLoads; ++s) {
-        const int fills = (ring_issued + kLoads - 1 - s) / kLoads;
-        if (fills) mbar_drain(bar(bLoadFull + s), (fills - 1) & 1);
-      }
+      for (int s = 0; s < kLoads; ++s)
+        if (ctl->fills[s]) mbar_drain(bar(bLoadFull + s), (ctl->fills[s] - 1) & 1);
     if (warp == 10 && lane == 0 && q_issued) mbar_drain(bar(B_FULLQ), (q_issued - 1) & 1);
     if (warp == 8 && elect_one()) {
       tc_commit(bar(B_DRAIN));
@@ -966,7 +980,7 @@ cudaError_t launch_tree(const LayerInfo &L, const CUtensorMap &tmq, const TreePa
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int ctas = P.groups * P.hkv;
-  k_tree_tc<D, F8><<<ctas, Gm::kThreads, smem, s>>>(L.tmk, L.tmv, tmq, P);
+  k_tree_tc<D, F8><<<ctas, kTreeThreads, smem, s>>>(L.tmk, L.tmv, tmq, P);
   e = cudaGetLastError();
   if (e != cudaSuccess || P.whole) return e;
   dim3 grid((rows + kMergeRows - 1) / kMergeRows, ctas);
