@@ -117,12 +117,24 @@ struct MergeDesc {
   int64_t q0;        // first query row
 };
 
-struct Segment {
-  int b, n0, n_tok, n_tiles;   // request (-1: end), first node, nodes, key tiles
-  int two;                     // two Q tiles (else one, key tiles alternate)
-  int part;                    // -1: whole item; else the partial's slot
+// A piece of the CTA's work.
+//   alternate  one Q tile; step u takes key tile u, the groups' accumulators are
+//              joined at the end
+//   shared     two Q tiles of one item, a key tile serves both groups
+//   pair       two whole items of one Q tile each, one per group, each with its
+//              own key tiles (the shorter one's are padded: masked, so 0)
+enum { kAlternate = 0, kShared = 1, kPair = 2 };
+struct Piece {                 // what a group works on
+  int b, n0, n_tok;            // request, first node, nodes
   int64_t q0, col0, prefix;    // first query row, first key column, cached columns
 };
+struct Segment {
+  int mode, n_tiles;           // mode -1: end; key tiles (of each piece)
+  int part;                    // -1: whole item; else the partial's slot
+  Piece piece[2];              // [1]: pairs only
+};
+// Key tiles that pass through the ring, in steps' order.
+__device__ __forceinline__ int ring_tiles(int mode, int n) { return mode == kPair ? 2 * n : n; }
 
 // Shared words of the roles.  (Everything lives in the dynamic array, whose
 // start is 1024-byte aligned: the tiles leave no room for an alignment gap.)
@@ -297,12 +309,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   auto load_q = [&](const Segment &sg, int nd) {
     if (nd >= 1 && !wait_all(bar(B_QFREE), (nd - 1) & 1)) return false;
     if (lane == 0) {
-      const int tiles = sg.two ? 2 : 1;
+      const int tiles = sg.mode == kAlternate ? 1 : 2;
       mbar_expect_tx(bar(B_FULLQ), (uint32_t)(tiles * TG * 128 * (kD / 64)));
-      for (int i = 0; i < tiles; ++i)
-        for (int h = 0; h < kD / 64; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        for (int h = 0; i < tiles && h < kD / 64; ++h)
           tma_load_3d(sb + i * kTileBytes + h * kBlock, &tmQ, h * 64, kvh * G,
-                      (int)(sg.q0 + i * T), bar(B_FULLQ));
+                      (int)(sg.mode == kPair && i ? sg.piece[1].q0 : sg.piece[0].q0 + i * T),
+                      bar(B_FULLQ));
       ++q_issued;
     }
     __syncwarp();
@@ -314,36 +328,38 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   const bool full_layer = P.kind == SWA_LAYER_FULL;
   const int ppt = kKeys >> P.ps_shift;       // pages per key tile
   auto stream = [&](const Segment &sg, int base, int kinds) {
-    const int32_t *rt_row = full_layer ? P.rt + P.req_idx[sg.b] * P.rt_stride : nullptr;
-    const int32_t *hdr = full_layer ? nullptr : P.plan.hdr + sg.b * 4;
-    const int32_t *pages = full_layer ? nullptr : P.plan.pages + (int64_t)sg.b * P.plan.max_pages;
-    const int64_t pg0 = sg.col0 >> P.ps_shift;
-    const int64_t hi = sg.prefix + sg.n0 + sg.n_tok - 1;   // the item's last column
-    // A windowed request's first page may start before its first planned
-    // column: look it up by a column that is in the plan.
-    const int64_t lo = full_layer ? 0 : first_position(P.kind, P.window, sg.prefix);
-    const int n_pg = (int)((hi >> P.ps_shift) - pg0 + 1);
-    const int n = sg.n_tiles, n_slots = n * ppt;
-    // Page slots behind the last column load its page again: finite values,
-    // zero weight.
-    auto rec_of = [&](int k) {
-      const int i = min(32 * k + lane, n_pg - 1);
+    const bool pair = sg.mode == kPair;
+    // Page records and rows of piece w: 32 page slots at a time, lane i slot i.
+    auto rec_of = [&](int w, int k) {
+      const Piece &pc = sg.piece[w];
+      const int64_t pg0 = pc.col0 >> P.ps_shift;
+      const int64_t hi = pc.prefix + pc.n0 + pc.n_tok - 1;   // the item's last column
+      // A windowed request's first page may start before its first planned
+      // column: look it up by a column that is in the plan.  Page slots behind
+      // the last column load its page again: finite values, zero weight.
+      const int64_t lo = full_layer ? 0 : first_position(P.kind, P.window, pc.prefix);
+      const int i = min(32 * k + lane, (int)((hi >> P.ps_shift) - pg0));
       const int64_t col = max((pg0 + i) << P.ps_shift, lo);
-      return page_rec(full_layer, P.ps_shift, rt_row, hdr, pages, col);
+      return page_rec(full_layer, P.ps_shift,
+                      full_layer ? P.rt + P.req_idx[pc.b] * P.rt_stride : nullptr,
+                      full_layer ? nullptr : P.plan.hdr + pc.b * 4,
+                      full_layer ? nullptr : P.plan.pages + (int64_t)pc.b * P.plan.max_pages, col);
     };
-    int32_t rows = page_row(P, full_layer, rec_of(0));   // of batch `cur`, lane i: slot i
-    int32_t rows_old = rows;                             // of the batch before
-    int32_t rec_next = n_slots > 32 ? rec_of(1) : 0;
+    const int n = ring_tiles(sg.mode, sg.n_tiles), n_slots = sg.n_tiles * ppt;
+    int32_t rows = page_row(P, full_layer, rec_of(0, 0));   // of batch `cur`
+    int32_t rows_old = rows;                                // of the batch before; a pair's second
+    if (pair) rows_old = page_row(P, full_layer, rec_of(1, 0));
+    int32_t rec_next = !pair && n_slots > 32 ? rec_of(0, 1) : 0;
     int cur = 0;
-    auto load_tile = [&](int t, int pos, const CUtensorMap *map) {
-      const int i0 = t * ppt;
-      if ((i0 >> 5) > cur) {
+    auto load_tile = [&](int x, int pos, const CUtensorMap *map) {
+      const int i0 = (pair ? x >> 1 : x) * ppt;
+      if (!pair && (i0 >> 5) > cur) {
         ++cur;
         rows_old = rows;
         rows = page_row(P, full_layer, rec_next);
-        rec_next = 32 * (cur + 1) < n_slots ? rec_of(cur + 1) : 0;
+        rec_next = 32 * (cur + 1) < n_slots ? rec_of(0, cur + 1) : 0;
       }
-      const int32_t held = (i0 >> 5) == cur ? rows : rows_old;
+      const int32_t held = (pair ? (x & 1) == 0 : (i0 >> 5) == cur) ? rows : rows_old;
       int32_t row[8];                        // first rows of the tile's pages
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -394,6 +410,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       ++n_pub;
       return true;
     };
+    Piece held{};                            // the first item of a pair, and its tiles
+    int held_n = 0;
+    auto emit = [&](int mode, int n, int part, const Piece &p0, const Piece &p1) {
+      Segment sg;
+      sg.mode = mode;
+      sg.n_tiles = n;
+      sg.part = part;
+      sg.piece[0] = p0;
+      sg.piece[1] = p1;
+      const bool good = publish(sg) && stream(sg, base, kF8 ? 3 : 1);
+      base += 2 * ring_tiles(mode, n);
+      return good;
+    };
+
     // The head's line of tiles (or items), and this CTA's stretch of it.
     int64_t total = 0;
     for (int b0 = 0; b0 < P.bs; b0 += 32) total += request(P, b0 + lane).tiles;
@@ -426,42 +456,51 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const int64_t len = block_tiles(P, q, blk), e = s + len;
           if (e > w0) {
             const int64_t from = max(s, w0), to = min(e, w1);
-            Segment sg;
-            sg.b = b0 + l;
-            sg.n0 = blk * 2 * T;
-            sg.n_tok = min(2 * T, q.n - sg.n0);
-            sg.two = sg.n_tok > T;
-            sg.q0 = q.q0 + sg.n0;
-            sg.prefix = q.prefix;
-            sg.col0 = q.col0;
-            const int64_t hi = q.prefix + sg.n0 + sg.n_tok - 1;
-            sg.part = -1;
-            if (P.whole) {
-              sg.n_tiles = (int)(((hi - q.col0) >> 7) + 1);
-            } else {
-              sg.n_tiles = (int)(to - from);
-              sg.col0 += (from - s) * kKeys;
+            Piece pc;
+            pc.b = b0 + l;
+            pc.n0 = blk * 2 * T;
+            pc.n_tok = min(2 * T, q.n - pc.n0);
+            pc.q0 = q.q0 + pc.n0;
+            pc.prefix = q.prefix;
+            pc.col0 = q.col0;
+            const bool one = pc.n_tok <= T;  // one Q tile
+            const int64_t hi = q.prefix + pc.n0 + pc.n_tok - 1;
+            int n = (int)(((hi - q.col0) >> 7) + 1), part = -1;
+            if (!P.whole) {
+              n = (int)(to - from);
+              pc.col0 += (from - s) * kKeys;
               if (from == s && to < e) {
-                sg.part = 1;
+                part = 1;
                 mine.parts = (int)((e - 1) / share) - group_id + 1;
-                mine.n_tok = sg.n_tok;
-                mine.q0 = sg.q0;
+                mine.n_tok = pc.n_tok;
+                mine.q0 = pc.q0;
               } else if (from > s) {
-                sg.part = 0;
+                part = 0;
               }
             }
-            ok = publish(sg) && stream(sg, base, kF8 ? 3 : 1);
-            base += 2 * sg.n_tiles;
+            // Whole items of one Q tile and few pages go in pairs.
+            if (P.whole && one && n * ppt <= 32) {
+              if (held_n) {
+                ok = emit(kPair, max(held_n, n), -1, held, pc);
+                held_n = 0;
+              } else {
+                held = pc;
+                held_n = n;
+              }
+            } else {
+              ok = emit(one ? kAlternate : kShared, n, part, pc, pc);
+            }
           }
           s = e;
         }
       }
       at += __shfl_sync(0xffffffffu, incl, 31);
     }
+    if (ok && held_n) ok = emit(kAlternate, held_n, -1, held, held);
     if (!P.whole && lane == 0) P.desc[blockIdx.x] = mine;
     if (ok) {
       Segment end{};
-      end.b = -1;
+      end.mode = -1;
       publish(end);
     }
   } else if (warp >= 10) {
@@ -474,8 +513,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const Segment sg = s_seg[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
-        if (sg.b < 0 || !(warp == 10 ? load_q(sg, nd) : stream(sg, base, 2))) break;
-        base += 2 * sg.n_tiles;
+        if (sg.mode < 0 || !(warp == 10 ? load_q(sg, nd) : stream(sg, base, 2))) break;
+        base += 2 * ring_tiles(sg.mode, sg.n_tiles);
       }
     } else {
       // ============ converters (E4M3 KV): Q, K and V to f16 ============
@@ -488,9 +527,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const Segment sg = s_seg[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
-        if (sg.b < 0 || (warp == 10 && !load_q(sg, nd))) break;
+        if (sg.mode < 0 || (warp == 10 && !load_q(sg, nd))) break;
         if (!wait_all(bar(B_FULLQ), nd & 1)) break;
-        const int q_chunks = (sg.two ? 2 : 1) * kTileBytes / 16;
+        const int q_chunks = (sg.mode == kAlternate ? 1 : 2) * kTileBytes / 16;
 #pragma unroll 4
         for (int i = ct; i < q_chunks; i += kConvThreads) {
           uint4 *q16 = reinterpret_cast<uint4 *>(smem + i * 16);
@@ -503,7 +542,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         fence_async_smem();                  // read by the tensor core (the async proxy)
         mbar_arrive(bar(B_QCONV));
-        for (int j = 0; j < 2 * sg.n_tiles; ++j, ++pos) {
+        for (int j = 0; j < 2 * ring_tiles(sg.mode, sg.n_tiles); ++j, ++pos) {
           const int rs = pos % kLoads, s = pos % kStages;
           if (!(ok = wait_all(bar(B_RAWFULL + rs), (pos / kLoads) & 1))) break;
           if (pos >= kStages && !(ok = wait_all(bar(B_EMPTY + s), (pos / kStages - 1) & 1))) break;
@@ -543,8 +582,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
   } else if (warp == 8) {
     // ===================== MMA issue =====================
-    // Step u of a segment belongs to softmax group u & 1 and key tile u / 2 (two
-    // Q tiles) or u; the order is S(0), S(1), then per step O(u), S(u + 2).  An
+    // Step u of a segment belongs to softmax group u & 1 and the ring's tile u / 2
+    // (shared) or u; the order is S(0), S(1), then per step O(u), S(u + 2).  An
     // elected lane runs a segment's steps: with the segment's numbers made
     // uniform by a warp reduction, descriptors are computed in uniform registers
     // (in a branch on the lane number a product cost 67 cycles to issue, whatever
@@ -558,19 +597,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     for (int nd = 0;; ++nd) {
       const int slot = nd & 1;
       if (!wait_all(bar(B_IFULL + slot), (nd >> 1) & 1)) break;
-      const int n = uni(s_seg[slot].n_tiles), two = uni(s_seg[slot].two), b = uni(s_seg[slot].b);
+      const int mode = uni(s_seg[slot].mode), tiles = uni(s_seg[slot].n_tiles);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
-      if (b < 0) break;
-      const int U = two ? 2 * n : n;
+      if (mode < 0) break;
+      const int U = mode == kAlternate ? tiles : 2 * tiles, n = ring_tiles(mode, tiles);
+      const bool shared = mode == kShared;   // a K/V tile serves two steps
       if (!wait_all(bar(kF8 ? B_QCONV : B_FULLQ), nd & 1)) break;
       int ok = 1;
       if (elect_one()) {
         for (int u = -2; u < U; ++u) {       // u = -2, -1: S(0) and S(1) only
           const int g = u & 1;
           if (u >= 0) {
-            const int t = two ? u >> 1 : u;
-            const int r = base + seq_v(t, n), s = r % kStages;
+            const int r = base + seq_v(shared ? u >> 1 : u, n), s = r % kStages;
             if (!(ok = mbar_wait(bar(B_FULL + s), (r / kStages) & 1, &s_abort))) break;
             if (!(ok = mbar_wait(bar(B_PREADY + g), ((g ? steps1 : steps0) + (u >> 1)) & 1, &s_abort)))
               break;
@@ -580,23 +619,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             for (int ks = 0; ks < kKeys / 16; ++ks)
               mma_ts(tmem + 256 + g * kD, tmem + g * 128 + ks * 8,
                      vd + (uint64_t)(ks * 16 * 128 >> 4), kIdO, (u >= 2 || ks > 0) ? 1u : 0u);
-            if (!two || g) tc_commit(bar(B_EMPTY + s));
+            if (!shared || g) tc_commit(bar(B_EMPTY + s));
             if (u + 2 >= U) tc_commit(bar(B_ODONE + g));
             if (U == 1) tc_commit(bar(B_ODONE + 1));
           }
           if (u + 2 < U) {                   // S(u + 2), of the same group
-            const int r = base + seq_k(two ? (u + 2) >> 1 : u + 2), s = r % kStages;
+            const int r = base + seq_k(shared ? (u + 2) >> 1 : u + 2), s = r % kStages;
             if (!(ok = mbar_wait(bar(B_FULL + s), (r / kStages) & 1, &s_abort))) break;
             tc_fence_after();
             const uint64_t kd = dk + (uint64_t)(s * kTileBytes >> 4);
-            const uint64_t qd = dq + (uint64_t)((two && g ? kTileBytes : 0) >> 4);
+            const uint64_t qd = dq + (uint64_t)((mode != kAlternate && g ? kTileBytes : 0) >> 4);
 #pragma unroll
             for (int ks = 0; ks < kD / 16; ++ks) {
               const uint64_t off = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
               mma_ss(tmem + g * 128, qd + off, kd + off, kIdS, ks > 0);
             }
             tc_commit(bar(B_SDONE + g));
-            if (!two || g) tc_commit(bar(B_EMPTY + s));
+            if (!shared || g) tc_commit(bar(B_EMPTY + s));
             if (u + 3 == U) tc_commit(bar(B_QFREE));
           }
         }
@@ -621,24 +660,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     for (int nd = 0;; ++nd) {
       const int slot = nd & 1;
       if (!wait_all(bar(B_IFULL + slot), (nd >> 1) & 1)) break;
-      const Segment sg = s_seg[slot];
+      const int mode = s_seg[slot].mode, n_tiles = s_seg[slot].n_tiles, part_slot = s_seg[slot].part;
+      const Piece pc = s_seg[slot].piece[mode == kPair ? grp : 0];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
-      if (sg.b < 0) break;
-      const int two = sg.two;
-      const int tr = (two ? grp * T : 0) + r / G;      // node of the item
-      const bool row_valid = r < TG && tr < sg.n_tok;
+      if (mode < 0) break;
+      const bool alone = mode != kAlternate;           // this group's rows are its own
+      const int tr = (mode == kShared ? grp * T : 0) + r / G;      // node of the item
+      const bool row_valid = r < TG && tr < pc.n_tok;
       const bool any_row = __any_sync(0xffffffffu, row_valid);
-      const uint32_t *row = P.tree.mask + (sg.q0 + (row_valid ? tr : 0)) * P.tree.words;
+      const uint32_t *row = P.tree.mask + (pc.q0 + (row_valid ? tr : 0)) * P.tree.words;
       int64_t lo_row = 0;
       if (row_valid) {
-        const int depth = P.tree.depth[sg.q0 + tr];
-        lo_row = tree_first_col(first_position(P.kind, P.window, sg.prefix + depth), sg.prefix,
-                                sg.n0 + tr, depth, row);
+        const int depth = P.tree.depth[pc.q0 + tr];
+        lo_row = tree_first_col(first_position(P.kind, P.window, pc.prefix + depth), pc.prefix,
+                                pc.n0 + tr, depth, row);
       }
       float m_run = row_valid ? -INFINITY : 0.f, l_run = 0.f;
       bool alive = true, first = true;
-      for (int t = two ? 0 : grp; t < sg.n_tiles; t += two ? 1 : 2) {
+      for (int t = alone ? 0 : grp; t < n_tiles; t += alone ? 1 : 2) {
         if (!wait_all(bar(B_SDONE + grp), steps & 1)) {
           alive = false;
           break;
@@ -648,16 +688,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         uint64_t acc2[2] = {0ull, 0ull};
 #pragma unroll 1
         for (int cb = 0; any_row && cb < 2; ++cb) {
-          const int64_t c0 = sg.col0 + (int64_t)t * kKeys + cb * 64;   // the chunk's first column
+          const int64_t c0 = pc.col0 + (int64_t)t * kKeys + cb * 64;   // the chunk's first column
           // Columns of the chunk this row reads.
-          const bool edge = row_valid && !(c0 >= lo_row && c0 + 64 <= sg.prefix);
+          const bool edge = row_valid && !(c0 >= lo_row && c0 + 64 <= pc.prefix);
           uint64_t allow = row_valid ? ~0ull : 0ull;
           const bool any_edge = __any_sync(0xffffffffu, edge);
           if (any_edge) {
             if (edge)
-              allow = bit_range(lo_row - c0, sg.prefix - c0) |
-                      (c0 + 64 > sg.prefix ? row_bits(row, P.tree.words, c0 - sg.prefix) &
-                                                 bit_range(max(lo_row, sg.prefix) - c0, 64)
+              allow = bit_range(lo_row - c0, pc.prefix - c0) |
+                      (c0 + 64 > pc.prefix ? row_bits(row, P.tree.words, c0 - pc.prefix) &
+                                                 bit_range(max(lo_row, pc.prefix) - c0, 64)
                                            : 0ull);
             if (!__any_sync(0xffffffffu, allow != 0ull)) {
               uint32_t zero[32];
@@ -774,7 +814,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // ---- epilogue ----
       if (!wait_all(bar(B_ODONE + grp), nd & 1)) break;
       float w0 = 1.f, w1 = 0.f;              // weights of this group's and the other's O
-      if (!two) {
+      if (!alone) {
         // Join the groups' halves of the keys: row statistics through shared
         // memory, accumulators read from TMEM; group i writes half i of D.
         s_stat[grp * kTileRows + r] = make_float2(m_run, l_run);
@@ -790,7 +830,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       tc_fence_after();
       float f = 1.f;
-      if (sg.part < 0) {
+      if (part_slot < 0) {
         const float mr = m_run == -INFINITY ? 0.f : m_run;
         const float mfin = fmaxf(mr, sg2);
         const float rsc = exp2f(mr - mfin);
@@ -799,21 +839,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       w0 *= f;
       w1 *= f;
-      const int row_i = (two ? grp * TG : 0) + r;      // row of the item
-      float *part = sg.part < 0 ? nullptr
-                                : P.partials + ((int64_t)blockIdx.x * 2 + sg.part) * P.part_stride;
+      const int row_i = (mode == kShared ? grp * TG : 0) + r;      // row of the item
+      float *part = part_slot < 0 ? nullptr
+                                : P.partials + ((int64_t)blockIdx.x * 2 + part_slot) * P.part_stride;
       const int rows_max = (int)(P.part_stride / (kD + 2));
-      if (part && row_valid && (two || grp == 0))
+      if (part && row_valid && (alone || grp == 0))
         reinterpret_cast<float2 *>(part + (int64_t)rows_max * kD)[row_i] = make_float2(m_run, l_run);
-      __nv_bfloat16 *orow = P.out + ((sg.q0 + tr) * (int64_t)(P.hkv * G) + head) * kD;
-      const int d_lo = two ? 0 : grp * (kD / 2), d_hi = two ? kD : d_lo + kD / 2;
+      __nv_bfloat16 *orow = P.out + ((pc.q0 + tr) * (int64_t)(P.hkv * G) + head) * kD;
+      const int d_lo = alone ? 0 : grp * (kD / 2), d_hi = alone ? kD : d_lo + kD / 2;
       const uint32_t tO2 = tmem + 256 + (grp ^ 1) * kD + lane_off;
       __syncwarp();
 #pragma unroll 1
       for (int d = d_lo; any_row && d < d_hi; d += 32) {
         uint32_t a[32];
         TC_LD32(tO + d, a);
-        if (two) {
+        if (alone) {
           tc_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * w0);
@@ -848,7 +888,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         __syncwarp();   // the TMEM loads are warp-collective
       }
       __syncwarp();
-      if (!two) {
+      if (!alone) {
         // Both groups have read both accumulators (and the statistics) before
         // the next segment's products overwrite them.
         tc_fence_before();
