@@ -41,10 +41,10 @@
 //     that one group's softmax overlaps the other's products, and the two
 //     accumulators are joined in TMEM's own lanes at the segment's end (warps i
 //     and i + 4 can read the same lanes).
-// E4M3 KV: K and V tiles arrive as bytes in a ring of their own; warps 10 and 11
-// turn them into f16 tiles (exact: E4M3 is a subset of f16) and each Q tile,
-// which they also load, from bf16 to f16 in place (12 warps in all: a 13th would
-// cost every thread a quarter of its registers); the products run on f16 operands, P is packed as f16,
+// E4M3 KV: K and V tiles arrive as bytes in a ring of their own; four more warps
+// turn them into f16 tiles (exact: E4M3 is a subset of f16) and each Q tile from
+// bf16 to f16 in place (with 16 warps the launch has 128 registers a thread, of
+// which the other roles give the softmax groups forty each: setmaxnreg); the products run on f16 operands, P is packed as f16,
 // the K scale joins the softmax scale and the V scale the output.
 // Key columns that some row may not read (window edge, non-ancestors) get -inf
 // scores from a 64-bit mask per row and 64-column chunk; chunks that no row of
@@ -70,7 +70,7 @@ constexpr int kTileRows = 128;               // rows of a Q tile (M)
 constexpr int kKeys = 128;                   // keys of a K/V tile
 constexpr int kBlock = kTileRows * 64 * 2;   // one 64-column block of a tile
 constexpr int kTreeThreads = 384;            // 8 softmax warps, MMA, and three that load
-constexpr int kConvThreads = 64;             // E4M3 KV: warps 10 and 11 convert
+constexpr int kConvThreads = 128;            // E4M3 KV: warps 12-15 convert
 constexpr float kRescaleGap = 8.f;           // log2 units: rescale O when the max grows more
 constexpr float kSumCap = 32768.f;           // a chunk's weight sum that forces a maximum pass
 constexpr int kMergeThreads = 128;
@@ -87,6 +87,7 @@ struct TreeGeo {
   static constexpr int kOffStat = kOffRaw + kRawStages * kRawBytes;
   static constexpr int kOffBars = kOffStat + 2 * kTileRows * 8;
   static constexpr int kOffCtl = kOffBars + 40 * 8;           // Control
+  static constexpr int kThreads = kTreeThreads + (F8 ? kConvThreads : 0);
 };
 
 struct TreeParams {
@@ -206,20 +207,23 @@ __device__ __forceinline__ int32_t page_row(const TreeParams &P, bool full, int3
 }
 
 // Bits [x, y) of a 64-bit mask, clipped to it.
-__device__ __forceinline__ uint64_t bit_range(int64_t x, int64_t y) {
-  x = max(x, (int64_t)0);
-  y = min(y, (int64_t)64);
-  if (x >= y) return 0ull;
-  return (~0ull >> (64 - (int)(y - x))) << (int)x;
+__device__ __forceinline__ uint64_t bit_range(int x, int y) {
+  x = max(x, 0);
+  y = min(y, 64);
+  return x < y ? (~0ull >> (64 - (y - x))) << x : 0ull;
 }
-// Bits o .. o + 63 of an ancestor row (o may be negative; zeros outside).
-__device__ __forceinline__ uint64_t row_bits(const uint32_t *row, int words, int64_t o) {
-  const int64_t w = o >> 5;
-  const int s = (int)(o & 31);
+// Bits o .. o + 63 of an ancestor row of more than 64 bits (o may be negative;
+// zeros outside).
+__device__ __forceinline__ uint64_t row_bits(const uint32_t *row, int words, int o) {
+  const int w = o >> 5, s = o & 31;
   uint32_t x[3];
 #pragma unroll
   for (int i = 0; i < 3; ++i) x[i] = (w + i >= 0 && w + i < words) ? row[w + i] : 0u;
   return (uint64_t)__funnelshift_r(x[0], x[1], s) | (uint64_t)__funnelshift_r(x[1], x[2], s) << 32;
+}
+// The same of a row of at most 64 bits.
+__device__ __forceinline__ uint64_t shift_bits(uint64_t row, int o) {
+  return o >= 64 || o <= -64 ? 0ull : o >= 0 ? row >> o : row << -o;
 }
 
 // (row r, 16-byte chunk c) of an operand tile: blocks of [128 rows][128 B] with the
@@ -229,7 +233,7 @@ __device__ __forceinline__ int tile_off(int r, int c) {
 }
 
 template <int kD, bool kF8>
-__global__ void __launch_bounds__(kTreeThreads, 1)
+__global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     k_tree_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
               const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TreeParams P) {
   using Gm = TreeGeo<kD, kF8>;
@@ -272,8 +276,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_IFULL + i), 1);
-      // 8 softmax warps, the MMA warp, and Q and V loaders or two converters
-      mbar_init(bar(B_IEMPTY + i), 11);
+      // 8 softmax warps, the MMA warp, the Q and V loaders (and four converters)
+      mbar_init(bar(B_IEMPTY + i), kF8 ? 15 : 11);
       mbar_init(bar(B_SDONE + i), 1);
       mbar_init(bar(B_PREADY + i), kTileRows);
       mbar_init(bar(B_ODONE + i), 1);
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     for (int i = 0; i < Gm::kRawStages; ++i) {
       mbar_init(bar(B_RAWFULL + i), 1);
-      mbar_init(bar(B_RAWEMPTY + i), 2);
+      mbar_init(bar(B_RAWEMPTY + i), kConvThreads / 32);
     }
     mbar_init(bar(B_QCONV), kConvThreads);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -323,11 +327,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     return true;
   };
 
-  // Warp-collective: the K tiles, the V tiles or both (kinds 1, 2, 3) of a
-  // segment whose first tile has position `base` in the ring of the loads.
+  // Warp-collective: the K tiles (warp 9) or the V tiles (warp 11) of a segment
+  // whose first tile has position `base` in the ring of the loads.
   const bool full_layer = P.kind == SWA_LAYER_FULL;
   const int ppt = kKeys >> P.ps_shift;       // pages per key tile
-  auto stream = [&](const Segment &sg, int base, int kinds) {
+  auto stream = [&](const Segment &sg, int base) {
     const bool pair = sg.mode == kPair;
     // Page records and rows of piece w: 32 page slots at a time, lane i slot i.
     auto rec_of = [&](int w, int k) {
@@ -347,19 +351,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     };
     const int n = ring_tiles(sg.mode, sg.n_tiles), n_slots = sg.n_tiles * ppt;
     int32_t rows = page_row(P, full_layer, rec_of(0, 0));   // of batch `cur`
-    int32_t rows_old = rows;                                // of the batch before; a pair's second
-    if (pair) rows_old = page_row(P, full_layer, rec_of(1, 0));
+    int32_t rows_two = rows;                                // a pair's second piece
+    if (pair) rows_two = page_row(P, full_layer, rec_of(1, 0));
     int32_t rec_next = !pair && n_slots > 32 ? rec_of(0, 1) : 0;
     int cur = 0;
     auto load_tile = [&](int x, int pos, const CUtensorMap *map) {
       const int i0 = (pair ? x >> 1 : x) * ppt;
       if (!pair && (i0 >> 5) > cur) {
         ++cur;
-        rows_old = rows;
         rows = page_row(P, full_layer, rec_next);
         rec_next = 32 * (cur + 1) < n_slots ? rec_of(0, cur + 1) : 0;
       }
-      const int32_t held = (pair ? (x & 1) == 0 : (i0 >> 5) == cur) ? rows : rows_old;
+      const int32_t held = !pair || (x & 1) == 0 ? rows : rows_two;
       int32_t row[8];                        // first rows of the tile's pages
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -385,16 +388,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       __syncwarp();
       return true;
     };
-    // In ring order; K runs one tile ahead of V.
-    for (int t = 0; t <= n; ++t) {
-      if ((kinds & 1) && t < n && !load_tile(t, base + seq_k(t), &tmK)) return false;
-      if ((kinds & 2) && t > 0 && !load_tile(t - 1, base + seq_v(t - 1, n), &tmV)) return false;
-    }
+    for (int t = 0; t < n; ++t)
+      if (!load_tile(t, base + (warp == 9 ? seq_k(t) : seq_v(t, n)), warp == 9 ? &tmK : &tmV))
+        return false;
     return true;
   };
 
+  if (warp >= 8) {
+  // E4M3 KV: 512 threads x 128 registers = 256 x 152 (softmax) + 256 x 104; whole
+  // warpgroups on each side.
+  if constexpr (kF8) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;\n");
   if (warp == 9) {
-    // ===================== producer: segments, K tiles (E4M3 KV: and V) =====================
+    // ===================== producer: segments, K tiles =====================
     int n_pub = 0, base = 0;                 // segments published; ring position
 
     bool ok = true;
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       sg.part = part;
       sg.piece[0] = p0;
       sg.piece[1] = p1;
-      const bool good = publish(sg) && stream(sg, base, kF8 ? 3 : 1);
+      const bool good = publish(sg) && stream(sg, base);
       base += 2 * ring_tiles(mode, n);
       return good;
     };
@@ -503,22 +508,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       end.mode = -1;
       publish(end);
     }
-  } else if (warp >= 10) {
-    if constexpr (!kF8) {
-      // ===================== Q tiles (warp 10), V tiles (warp 11) =====================
-      int base = 0;
-      for (int nd = 0;; ++nd) {
-        const int slot = nd & 1;
-        if (!wait_all(bar(B_IFULL + slot), (nd >> 1) & 1)) break;
-        const Segment sg = s_seg[slot];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
-        if (sg.mode < 0 || !(warp == 10 ? load_q(sg, nd) : stream(sg, base, 2))) break;
-        base += 2 * ring_tiles(sg.mode, sg.n_tiles);
-      }
-    } else {
+  } else if (warp == 10 || warp == 11) {
+    // ===================== Q tiles (warp 10), V tiles (warp 11) =====================
+    int base = 0;
+    for (int nd = 0;; ++nd) {
+      const int slot = nd & 1;
+      if (!wait_all(bar(B_IFULL + slot), (nd >> 1) & 1)) break;
+      const Segment sg = s_seg[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
+      if (sg.mode < 0 || !(warp == 10 ? load_q(sg, nd) : stream(sg, base))) break;
+      base += 2 * ring_tiles(sg.mode, sg.n_tiles);
+    }
+  } else if (warp >= 12) {
+    if constexpr (kF8) {
       // ============ converters (E4M3 KV): Q, K and V to f16 ============
-      const int ct = tid - 320;              // 0 .. 63
+      const int ct = tid - kTreeThreads;     // 0 .. 127
       int pos = 0;                           // ring position, both rings
       bool ok = true;
       for (int nd = 0; ok; ++nd) {
@@ -527,7 +532,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const Segment sg = s_seg[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
-        if (sg.mode < 0 || (warp == 10 && !load_q(sg, nd))) break;
+        if (sg.mode < 0) break;
         if (!wait_all(bar(B_FULLQ), nd & 1)) break;
         const int q_chunks = (sg.mode == kAlternate ? 1 : 2) * kTileBytes / 16;
 #pragma unroll 4
@@ -552,26 +557,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           // the other halves): neither the reads of 16 E4M3 values nor the two
           // 16-byte writes that they become meet in a bank.
           const int odd = (ct >> 2) & 1;
+          uint4 w[8];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = ((h ^ odd) << 2) + (ct & 3);
-            uint4 w[8];
+          for (int i = 0; i < 8; ++i) {
+            const int c = (((i & 1) ^ odd) << 2) + (ct & 3);
+            const int r = 2 * ((i >> 1) * 16 + (ct >> 3)) + odd;
+            w[i] = *reinterpret_cast<const uint4 *>(src + r * 128 + ((c ^ (r & 7)) << 4));
+          }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = 2 * (i * 8 + (ct >> 3)) + odd;
-              w[i] = *reinterpret_cast<const uint4 *>(src + r * 128 + ((c ^ (r & 7)) << 4));
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = 2 * (i * 8 + (ct >> 3)) + odd;
-              uint4 a, b;
-              e4m3x4_to_f16x4(w[i].x, a.x, a.y);
-              e4m3x4_to_f16x4(w[i].y, a.z, a.w);
-              e4m3x4_to_f16x4(w[i].z, b.x, b.y);
-              e4m3x4_to_f16x4(w[i].w, b.z, b.w);
-              *reinterpret_cast<uint4 *>(dst + tile_off(r, 2 * c)) = a;
-              *reinterpret_cast<uint4 *>(dst + tile_off(r, 2 * c + 1)) = b;
-            }
+          for (int i = 0; i < 8; ++i) {
+            const int c = (((i & 1) ^ odd) << 2) + (ct & 3);
+            const int r = 2 * ((i >> 1) * 16 + (ct >> 3)) + odd;
+            uint4 a, b;
+            e4m3x4_to_f16x4(w[i].x, a.x, a.y);
+            e4m3x4_to_f16x4(w[i].y, a.z, a.w);
+            e4m3x4_to_f16x4(w[i].z, b.x, b.y);
+            e4m3x4_to_f16x4(w[i].w, b.z, b.w);
+            *reinterpret_cast<uint4 *>(dst + tile_off(r, 2 * c)) = a;
+            *reinterpret_cast<uint4 *>(dst + tile_off(r, 2 * c + 1)) = b;
           }
           fence_async_smem();
           mbar_arrive(bar(B_FULL + s));
@@ -645,7 +648,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       steps1 += U >> 1;
       base += 2 * n;
     }
-  } else if (warp < 8) {
+  }
+  } else {
+    if constexpr (kF8) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;\n");
     // ===================== softmax group =====================
     const int grp = warp >> 2;
     const int r = tid & 127;                 // row of the Q tile = TMEM lane
@@ -670,11 +675,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const bool row_valid = r < TG && tr < pc.n_tok;
       const bool any_row = __any_sync(0xffffffffu, row_valid);
       const uint32_t *row = P.tree.mask + (pc.q0 + (row_valid ? tr : 0)) * P.tree.words;
-      int64_t lo_row = 0;
+      // Relative to the piece's first column: the row's first column, and the
+      // first behind the cached ones.  Rows of at most 64 nodes keep their
+      // ancestors in a register.
+      const bool few = P.tree.words <= 2;
+      int lo_row = 0;
+      const int behind = (int)min(pc.prefix - pc.col0, (int64_t)1 << 30);
+      uint64_t above = 0ull;
       if (row_valid) {
         const int depth = P.tree.depth[pc.q0 + tr];
-        lo_row = tree_first_col(first_position(P.kind, P.window, pc.prefix + depth), pc.prefix,
-                                pc.n0 + tr, depth, row);
+        if (few) above = row[0] | (P.tree.words == 2 ? (uint64_t)row[1] << 32 : 0ull);
+        const int64_t lo = tree_first_col(first_position(P.kind, P.window, pc.prefix + depth),
+                                          pc.prefix, pc.n0 + tr, depth, row);
+        lo_row = (int)max(lo - pc.col0, -((int64_t)1 << 30));
       }
       float m_run = row_valid ? -INFINITY : 0.f, l_run = 0.f;
       bool alive = true, first = true;
@@ -688,17 +701,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         uint64_t acc2[2] = {0ull, 0ull};
 #pragma unroll 1
         for (int cb = 0; any_row && cb < 2; ++cb) {
-          const int64_t c0 = pc.col0 + (int64_t)t * kKeys + cb * 64;   // the chunk's first column
+          const int c0 = t * kKeys + cb * 64;        // the chunk's first column
           // Columns of the chunk this row reads.
-          const bool edge = row_valid && !(c0 >= lo_row && c0 + 64 <= pc.prefix);
+          const bool edge = row_valid && !(c0 >= lo_row && c0 + 64 <= behind);
           uint64_t allow = row_valid ? ~0ull : 0ull;
           const bool any_edge = __any_sync(0xffffffffu, edge);
           if (any_edge) {
-            if (edge)
-              allow = bit_range(lo_row - c0, pc.prefix - c0) |
-                      (c0 + 64 > pc.prefix ? row_bits(row, P.tree.words, c0 - pc.prefix) &
-                                                 bit_range(max(lo_row, pc.prefix) - c0, 64)
-                                           : 0ull);
+            if (edge) {
+              allow = bit_range(lo_row - c0, behind - c0);
+              if (c0 + 64 > behind)
+                allow |= (few ? shift_bits(above, c0 - behind)
+                              : row_bits(row, P.tree.words, c0 - behind)) &
+                         bit_range(max(lo_row, behind) - c0, 64);
+            }
             if (!__any_sync(0xffffffffu, allow != 0ull)) {
               uint32_t zero[32];
 #pragma unroll
@@ -1020,7 +1035,7 @@ cudaError_t launch_tree(const LayerInfo &L, const CUtensorMap &tmq, const TreePa
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int ctas = P.groups * P.hkv;
-  k_tree_tc<D, F8><<<ctas, kTreeThreads, smem, s>>>(L.tmk, L.tmv, tmq, P);
+  k_tree_tc<D, F8><<<ctas, Gm::kThreads, smem, s>>>(L.tmk, L.tmv, tmq, P);
   e = cudaGetLastError();
   if (e != cudaSuccess || P.whole) return e;
   dim3 grid((rows + kMergeRows - 1) / kMergeRows, ctas);
