@@ -97,6 +97,7 @@ struct TreeParams {
   int64_t rt_stride;
   const int64_t *req_idx, *pre, *qo_indptr;
   int bs, groups, max_new;
+  int blocks;                // most blocks of 2 T nodes of a request
   int whole;                 // 1: CTAs take whole items, nothing is merged
   int64_t n_tokens;
   PlanView plan;
@@ -115,7 +116,7 @@ struct TreeParams {
 struct MergeDesc {
   int32_t parts;     // contributing CTAs (0: nothing to merge)
   int32_t n_tok;     // nodes of the item
-  int64_t q0;        // first query row
+  int32_t q0;        // first query row
 };
 
 // A piece of the CTA's work.
@@ -127,7 +128,7 @@ struct MergeDesc {
 enum { kAlternate = 0, kShared = 1, kPair = 2 };
 struct Piece {                 // what a group works on
   int b, n0, n_tok;            // request, first node, nodes
-  int64_t q0, col0, prefix;    // first query row, first key column, cached columns
+  int q0, col0, prefix;        // first query row, first key column, cached columns
 };
 struct Segment {
   int mode, n_tiles;           // mode -1: end; key tiles (of each piece)
@@ -157,33 +158,34 @@ __device__ __forceinline__ int seq_v(int i, int n) { return min(2 * i + 2, 2 * n
 
 // One request's nodes and keys as the schedule sees them.
 struct Request {
-  int64_t q0, prefix, col0, tiles;   // tiles: of all its blocks (items with `whole`)
-  int n, blocks;
+  int q0, prefix, col0, n;
 };
-__device__ __forceinline__ int64_t block_tiles(const TreeParams &P, const Request &r, int blk) {
-  if (P.whole) return 1;
+constexpr int kMaxCol = 0x7fffffff - 2 * SWA_TREE_MAX_NODES;
+__device__ __forceinline__ int n_blocks(const TreeParams &P, const Request &r) {
+  return (r.n + 2 * P.T - 1) / (2 * P.T);
+}
+// Key tiles of one of its blocks of nodes.
+__device__ __forceinline__ int block_tiles(const TreeParams &P, const Request &r, int blk) {
   const int last = min((blk + 1) * 2 * P.T, r.n);   // nodes up to the block's end
   return ((r.prefix + last - 1 - r.col0) >> 7) + 1;
 }
 __device__ __forceinline__ Request request(const TreeParams &P, int b) {
-  Request r;
-  r.q0 = r.prefix = r.col0 = r.tiles = 0;
-  r.n = r.blocks = 0;
+  Request r{0, 0, 0, 0};
   if (b >= P.bs) return r;
-  r.q0 = P.qo_indptr[b];
-  int64_t n = P.qo_indptr[b + 1] - r.q0;
-  r.prefix = P.pre[b];
+  const int64_t q0 = P.qo_indptr[b], end = P.qo_indptr[b + 1], prefix = P.pre[b];
+  int64_t n = end - q0;
   if (n <= 0) return r;
-  const int64_t room = P.kind == SWA_LAYER_FULL ? P.rt_stride - r.prefix : n;
-  if (r.q0 < 0 || r.q0 + n > P.n_tokens || n > P.max_new || r.prefix < 0 || n > room) {
+  const int64_t room =
+      (P.kind == SWA_LAYER_FULL && P.rt_stride < kMaxCol ? P.rt_stride : kMaxCol) - prefix;
+  if (q0 < 0 || end > P.n_tokens || n > P.max_new || prefix < 0 || n > room) {
     set_error(P.err, SWA_DEVERR_RANGE);
-    if (r.q0 < 0 || r.q0 >= P.n_tokens || r.prefix < 0 || room <= 0) return r;
-    n = min(min(n, P.n_tokens - r.q0), min((int64_t)P.max_new, room));
+    if (q0 < 0 || q0 >= P.n_tokens || prefix < 0 || room <= 0) return r;
+    n = min(min(n, P.n_tokens - q0), min((int64_t)P.max_new, room));
   }
+  r.q0 = (int)q0;
+  r.prefix = (int)prefix;
   r.n = (int)n;
-  r.blocks = (r.n + 2 * P.T - 1) / (2 * P.T);
-  r.col0 = first_position(P.kind, P.window, r.prefix) >> P.ps_shift << P.ps_shift;
-  for (int i = 0; i < r.blocks; ++i) r.tiles += block_tiles(P, r, i);
+  r.col0 = (int)first_position(P.kind, P.window, prefix) >> P.ps_shift << P.ps_shift;
   return r;
 }
 
@@ -191,10 +193,11 @@ __device__ __forceinline__ Request request(const TreeParams &P, int b) {
 // its req_to_token entry (full layers) or its page in the request's plan, -1
 // when the plan has none.  An offending page reads as page 0.
 __device__ __forceinline__ int32_t page_rec(bool full, int ps_shift, const int32_t *rt_row,
-                                            const int32_t *hdr, const int32_t *pages, int64_t col) {
+                                            const int32_t *hdr, const int32_t *pages, int col) {
   if (full) return rt_row[col];
-  const int64_t k = (col >> ps_shift) - hdr[2];
-  return (col >= hdr[0] && k >= 0 && k < hdr[3]) ? pages[k] : -1;
+  const int4 h = *reinterpret_cast<const int4 *>(hdr);   // lo, hi, first page, pages
+  const int k = (col >> ps_shift) - h.z;
+  return (col >= h.x && k >= 0 && k < h.w) ? pages[k] : -1;
 }
 __device__ __forceinline__ int32_t page_row(const TreeParams &P, bool full, int32_t rec) {
   int64_t page = full ? (rec >= 0 ? rec >> P.ps_shift : -1) : rec;
@@ -308,6 +311,12 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
 
   int q_issued = 0;                          // Q fills, for the abort path
 
+  // Launched as a programmatic dependent: what is above overlaps the kernel
+  // before this one on the stream, everything that reads or writes memory comes
+  // after its completion.
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+
   // Warp-collective, warp 10: the Q tiles of the CTA's segment nd, once the last
   // QK^T of the one before has read the buffers.
   auto load_q = [&](const Segment &sg, int nd) {
@@ -336,14 +345,14 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     // Page records and rows of piece w: 32 page slots at a time, lane i slot i.
     auto rec_of = [&](int w, int k) {
       const Piece &pc = sg.piece[w];
-      const int64_t pg0 = pc.col0 >> P.ps_shift;
-      const int64_t hi = pc.prefix + pc.n0 + pc.n_tok - 1;   // the item's last column
+      const int pg0 = pc.col0 >> P.ps_shift;
+      const int hi = pc.prefix + pc.n0 + pc.n_tok - 1;       // the item's last column
       // A windowed request's first page may start before its first planned
       // column: look it up by a column that is in the plan.  Page slots behind
       // the last column load its page again: finite values, zero weight.
-      const int64_t lo = full_layer ? 0 : first_position(P.kind, P.window, pc.prefix);
-      const int i = min(32 * k + lane, (int)((hi >> P.ps_shift) - pg0));
-      const int64_t col = max((pg0 + i) << P.ps_shift, lo);
+      const int lo = (int)first_position(P.kind, P.window, pc.prefix);
+      const int i = min(32 * k + lane, (hi >> P.ps_shift) - pg0);
+      const int col = max((pg0 + i) << P.ps_shift, lo);
       return page_rec(full_layer, P.ps_shift,
                       full_layer ? P.rt + P.req_idx[pc.b] * P.rt_stride : nullptr,
                       full_layer ? nullptr : P.plan.hdr + pc.b * 4,
@@ -429,51 +438,81 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       return good;
     };
 
-    // The head's line of tiles (or items), and this CTA's stretch of it.
-    int64_t total = 0;
-    for (int b0 = 0; b0 < P.bs; b0 += 32) total += request(P, b0 + lane).tiles;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const int64_t share = (total + P.groups - 1) / P.groups;
-    const int64_t w0 = group_id * share, w1 = min(total, w0 + share);
-    int64_t at = 0;                          // line position of the batch's first request
-    for (int b0 = 0; ok && b0 < P.bs && at < w1; b0 += 32) {
-      const Request r = request(P, b0 + lane);
-      int64_t incl = r.tiles;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+    auto bcast = [&](int x, int l) { return __shfl_sync(0xffffffffu, x, l); };
+    if (P.whole) {
+      // The head's line of blocks, every request's the same number of them (some
+      // empty), so nothing is summed up; this CTA's stretch of it, 32 at a time.
+      const int per = P.blocks;
+      const int64_t total = (int64_t)P.bs * per, share = (total + P.groups - 1) / P.groups;
+      const int64_t w0 = group_id * share, w1 = min(total, w0 + share);
+      for (int64_t x0 = w0; ok && x0 < w1; x0 += 32) {
+        const int64_t x = x0 + lane;
+        const int b = (int)(x / per), blk = (int)(x % per);
+        const Request r = request(P, x < w1 ? b : P.bs);
+        Piece mp{b, blk * 2 * T, min(2 * T, r.n - blk * 2 * T), r.q0 + blk * 2 * T, r.col0, r.prefix};
+        const int tiles = mp.n_tok > 0 ? block_tiles(P, r, blk) : 0;
+        unsigned hit = __ballot_sync(0xffffffffu, mp.n_tok > 0);
+        while (ok && hit) {
+          const int l = __ffs(hit) - 1;
+          hit &= hit - 1;
+          const Piece pc{bcast(mp.b, l),  bcast(mp.n0, l),   bcast(mp.n_tok, l),
+                         bcast(mp.q0, l), bcast(mp.col0, l), bcast(mp.prefix, l)};
+          const int n = bcast(tiles, l);
+          // Items of one Q tile and few pages go in pairs.
+          if (pc.n_tok <= T && n * ppt <= 32) {
+            if (held_n) {
+              ok = emit(kPair, max(held_n, n), -1, held, pc);
+              held_n = 0;
+            } else {
+              held = pc;
+              held_n = n;
+            }
+          } else {
+            ok = emit(pc.n_tok <= T ? kAlternate : kShared, n, -1, pc, pc);
+          }
+        }
       }
-      const int64_t s0 = at + incl - r.tiles;
-      unsigned hit = __ballot_sync(0xffffffffu, r.tiles > 0 && s0 < w1 && s0 + r.tiles > w0);
-      while (ok && hit) {
-        const int l = __ffs(hit) - 1;
-        hit &= hit - 1;
-        Request q;
-        q.q0 = __shfl_sync(0xffffffffu, r.q0, l);
-        q.prefix = __shfl_sync(0xffffffffu, r.prefix, l);
-        q.col0 = __shfl_sync(0xffffffffu, r.col0, l);
-        q.n = __shfl_sync(0xffffffffu, r.n, l);
-        q.blocks = __shfl_sync(0xffffffffu, r.blocks, l);
-        int64_t s = __shfl_sync(0xffffffffu, s0, l);
-        for (int blk = 0; ok && blk < q.blocks && s < w1; ++blk) {
-          const int64_t len = block_tiles(P, q, blk), e = s + len;
-          if (e > w0) {
-            const int64_t from = max(s, w0), to = min(e, w1);
-            Piece pc;
-            pc.b = b0 + l;
-            pc.n0 = blk * 2 * T;
-            pc.n_tok = min(2 * T, q.n - pc.n0);
-            pc.q0 = q.q0 + pc.n0;
-            pc.prefix = q.prefix;
-            pc.col0 = q.col0;
-            const bool one = pc.n_tok <= T;  // one Q tile
-            const int64_t hi = q.prefix + pc.n0 + pc.n_tok - 1;
-            int n = (int)(((hi - q.col0) >> 7) + 1), part = -1;
-            if (!P.whole) {
-              n = (int)(to - from);
-              pc.col0 += (from - s) * kKeys;
+    } else {
+      // The head's line of tiles, and this CTA's stretch of it.
+      auto tiles_of = [&](const Request &r) {
+        int64_t n = 0;
+        for (int i = 0; i < n_blocks(P, r); ++i) n += block_tiles(P, r, i);
+        return n;
+      };
+      int64_t total = 0;
+      for (int b0 = 0; b0 < P.bs; b0 += 64) {
+        const Request a = request(P, b0 + lane), b = request(P, b0 + 32 + lane);
+        total += tiles_of(a) + tiles_of(b);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      const int64_t share = (total + P.groups - 1) / P.groups;
+      const int64_t w0 = group_id * share, w1 = min(total, w0 + share);
+      int64_t at = 0;                        // line position of the batch's first request
+      for (int b0 = 0; ok && b0 < P.bs && at < w1; b0 += 32) {
+        const Request r = request(P, b0 + lane);
+        const int64_t mine_tiles = tiles_of(r);
+        int64_t incl = mine_tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        const int64_t s0 = at + incl - mine_tiles;
+        unsigned hit = __ballot_sync(0xffffffffu, mine_tiles > 0 && s0 < w1 && s0 + mine_tiles > w0);
+        while (ok && hit) {
+          const int l = __ffs(hit) - 1;
+          hit &= hit - 1;
+          const Request q{bcast(r.q0, l), bcast(r.prefix, l), bcast(r.col0, l), bcast(r.n, l)};
+          int64_t s = __shfl_sync(0xffffffffu, s0, l);
+          for (int blk = 0; ok && blk < n_blocks(P, q) && s < w1; ++blk) {
+            const int64_t e = s + block_tiles(P, q, blk);
+            if (e > w0) {
+              const int64_t from = max(s, w0), to = min(e, w1);
+              const int n0 = blk * 2 * T;
+              const Piece pc{b0 + l,     n0, min(2 * T, q.n - n0), q.q0 + n0,
+                             q.col0 + (int)(from - s) * kKeys, q.prefix};
+              int part = -1;
               if (from == s && to < e) {
                 part = 1;
                 mine.parts = (int)((e - 1) / share) - group_id + 1;
@@ -482,24 +521,13 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
               } else if (from > s) {
                 part = 0;
               }
+              ok = emit(pc.n_tok <= T ? kAlternate : kShared, (int)(to - from), part, pc, pc);
             }
-            // Whole items of one Q tile and few pages go in pairs.
-            if (P.whole && one && n * ppt <= 32) {
-              if (held_n) {
-                ok = emit(kPair, max(held_n, n), -1, held, pc);
-                held_n = 0;
-              } else {
-                held = pc;
-                held_n = n;
-              }
-            } else {
-              ok = emit(one ? kAlternate : kShared, n, part, pc, pc);
-            }
+            s = e;
           }
-          s = e;
         }
+        at += __shfl_sync(0xffffffffu, incl, 31);
       }
-      at += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (ok && held_n) ok = emit(kAlternate, held_n, -1, held, held);
     if (!P.whole && lane == 0) P.desc[blockIdx.x] = mine;
@@ -662,33 +690,56 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     const float sc = P.scale_log2;
     const uint64_t sc2 = f2pack(sc, sc);
     int steps = 0, joins = 0;
-    for (int nd = 0;; ++nd) {
+    // A segment as this row sees it, with what it loads of its node: taken from
+    // the ring before the previous segment's epilogue, which covers the loads.
+    struct Mine {
+      int mode, n_tiles, part, tr, depth;
+      Piece pc;
+      bool valid;
+      uint64_t above;          // ancestors, in trees of at most 64 nodes
+    };
+    const bool few = P.tree.words <= 2;
+    auto take = [&](int nd, Mine &m) {
       const int slot = nd & 1;
-      if (!wait_all(bar(B_IFULL + slot), (nd >> 1) & 1)) break;
-      const int mode = s_seg[slot].mode, n_tiles = s_seg[slot].n_tiles, part_slot = s_seg[slot].part;
-      const Piece pc = s_seg[slot].piece[mode == kPair ? grp : 0];
+      if (!wait_all(bar(B_IFULL + slot), (nd >> 1) & 1)) return false;
+      m.mode = s_seg[slot].mode;
+      m.n_tiles = s_seg[slot].n_tiles;
+      m.part = s_seg[slot].part;
+      m.pc = s_seg[slot].piece[m.mode == kPair ? grp : 0];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
-      if (mode < 0) break;
-      const bool alone = mode != kAlternate;           // this group's rows are its own
-      const int tr = (mode == kShared ? grp * T : 0) + r / G;      // node of the item
-      const bool row_valid = r < TG && tr < pc.n_tok;
-      const bool any_row = __any_sync(0xffffffffu, row_valid);
-      const uint32_t *row = P.tree.mask + (pc.q0 + (row_valid ? tr : 0)) * P.tree.words;
-      // Relative to the piece's first column: the row's first column, and the
-      // first behind the cached ones.  Rows of at most 64 nodes keep their
-      // ancestors in a register.
-      const bool few = P.tree.words <= 2;
-      int lo_row = 0;
-      const int behind = (int)min(pc.prefix - pc.col0, (int64_t)1 << 30);
-      uint64_t above = 0ull;
-      if (row_valid) {
-        const int depth = P.tree.depth[pc.q0 + tr];
-        if (few) above = row[0] | (P.tree.words == 2 ? (uint64_t)row[1] << 32 : 0ull);
-        const int64_t lo = tree_first_col(first_position(P.kind, P.window, pc.prefix + depth),
-                                          pc.prefix, pc.n0 + tr, depth, row);
-        lo_row = (int)max(lo - pc.col0, -((int64_t)1 << 30));
+      m.tr = (m.mode == kShared ? grp * T : 0) + r / G;       // node of the item
+      m.valid = m.mode >= 0 && r < TG && m.tr < m.pc.n_tok;
+      m.depth = 0;
+      m.above = 0ull;
+      if (m.valid) {
+        const uint32_t *row = P.tree.mask + (int64_t)(m.pc.q0 + m.tr) * P.tree.words;
+        m.depth = P.tree.depth[m.pc.q0 + m.tr];
+        if (few) m.above = row[0] | (P.tree.words == 2 ? (uint64_t)row[1] << 32 : 0ull);
       }
+      __syncwarp();
+      return true;
+    };
+    Mine next;
+    for (int nd = 0;; ++nd) {
+      if (nd == 0 && !take(0, next)) break;
+      const Mine cur = next;
+      if (cur.mode < 0) break;
+      const int mode = cur.mode, n_tiles = cur.n_tiles, tr = cur.tr, part_slot = cur.part;
+      const Piece pc = cur.pc;
+      const bool alone = mode != kAlternate;           // this group's rows are its own
+      const bool row_valid = cur.valid;
+      const uint64_t above = cur.above;
+      const bool any_row = __any_sync(0xffffffffu, row_valid);
+      const uint32_t *row = P.tree.mask + (int64_t)(pc.q0 + (row_valid ? tr : 0)) * P.tree.words;
+      // Relative to the piece's first column: the row's first column, and the
+      // first behind the cached ones.
+      int lo_row = 0;
+      const int behind = pc.prefix - pc.col0;
+      if (row_valid)
+        lo_row = (int)tree_first_col(first_position(P.kind, P.window, pc.prefix + cur.depth),
+                                     pc.prefix, pc.n0 + tr, cur.depth, row) -
+                 pc.col0;
       float m_run = row_valid ? -INFINITY : 0.f, l_run = 0.f;
       bool alive = true, first = true;
       for (int t = alone ? 0 : grp; t < n_tiles; t += alone ? 1 : 2) {
@@ -825,7 +876,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
         tc_fence_before();
         mbar_arrive(bar(B_PREADY + grp));
       }
-      if (!alive) break;
+      if (!alive || !take(nd + 1, next)) break;
       // ---- epilogue ----
       if (!wait_all(bar(B_ODONE + grp), nd & 1)) break;
       float w0 = 1.f, w1 = 0.f;              // weights of this group's and the other's O
@@ -860,7 +911,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       const int rows_max = (int)(P.part_stride / (kD + 2));
       if (part && row_valid && (alone || grp == 0))
         reinterpret_cast<float2 *>(part + (int64_t)rows_max * kD)[row_i] = make_float2(m_run, l_run);
-      __nv_bfloat16 *orow = P.out + ((pc.q0 + tr) * (int64_t)(P.hkv * G) + head) * kD;
+      __nv_bfloat16 *orow = P.out + ((int64_t)(pc.q0 + tr) * (P.hkv * G) + head) * kD;
       const int d_lo = alone ? 0 : grp * (kD / 2), d_hi = alone ? kD : d_lo + kD / 2;
       const uint32_t tO2 = tmem + 256 + (grp ^ 1) * kD + lane_off;
       __syncwarp();
@@ -943,6 +994,8 @@ template <int kD>
 __global__ void __launch_bounds__(kMergeThreads) k_tree_merge(const __grid_constant__ TreeParams P) {
   constexpr int kPer = kD / 32;              // floats per lane
   using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const MergeDesc d = P.desc[blockIdx.y];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kvh = blockIdx.y % P.hkv, G = P.G;
@@ -990,7 +1043,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_tree_merge(const __grid_const
     if (P.sinks) L += exp2f(sg2 - M);
     const float f = P.v_scale / L;
     __nv_bfloat16 *dst =
-        P.out + ((d.q0 + r / G) * (int64_t)(P.hkv * G) + head) * kD + lane * kPer;
+        P.out + ((int64_t)(d.q0 + r / G) * (P.hkv * G) + head) * kD + lane * kPer;
 #pragma unroll
     for (int e = 0; e < kPer; e += 2)
       *reinterpret_cast<uint32_t *>(dst + e) = pack_p<false>(acc[e] * f, acc[e + 1] * f);
@@ -1035,12 +1088,22 @@ cudaError_t launch_tree(const LayerInfo &L, const CUtensorMap &tmq, const TreePa
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int ctas = P.groups * P.hkv;
-  k_tree_tc<D, F8><<<ctas, Gm::kThreads, smem, s>>>(L.tmk, L.tmv, tmq, P);
-  e = cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(Gm::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, k_tree_tc<D, F8>, L.tmk, L.tmv, tmq, P);
   if (e != cudaSuccess || P.whole) return e;
-  dim3 grid((rows + kMergeRows - 1) / kMergeRows, ctas);
-  k_tree_merge<D><<<grid, kMergeThreads, 0, s>>>(P);
-  return cudaGetLastError();
+  cfg.gridDim = dim3((rows + kMergeRows - 1) / kMergeRows, ctas);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, k_tree_merge<D>, P);
 }
 
 }  // namespace
@@ -1078,6 +1141,7 @@ cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree,
   P.qo_indptr = a.qo_indptr;
   P.bs = a.bs;
   P.groups = w.groups;
+  P.blocks = (a.max_new + 2 * P.T - 1) / (2 * P.T);
   P.max_new = a.max_new;
   P.whole = w.whole ? 1 : 0;
   P.n_tokens = a.nq;

@@ -760,8 +760,8 @@ swa_status swa_tree_plan(swa_ctx *c, int32_t bs, const int32_t *parents,
   if (bs == 0 || n_tokens == 0) return SWA_OK;
   if (!parents || !prefix_lens || !qo_indptr || !tree)
     return fail(c, SWA_ERR_INVALID, "bad tree plan args");
-  if (tree_bytes < swa_tree_bytes(c, n_tokens, max_new))
-    return fail(c, SWA_ERR_INVALID, "tree buffer too small");
+  if (tree_bytes < swa_tree_bytes(c, n_tokens, max_new) || (reinterpret_cast<uintptr_t>(tree) & 15))
+    return fail(c, SWA_ERR_INVALID, "tree buffer too small or not 16-byte aligned");
   CUDA_TRY(c, swa::launch_tree_plan(*c, bs, parents, prefix_lens, qo_indptr, n_tokens, max_new,
                                     positions, swa::tree_view(tree, n_tokens, max_new),
                                     (cudaStream_t)stream));
@@ -799,8 +799,10 @@ swa_status swa_attn_tree(swa_ctx *c, int32_t layer, int32_t bs, const int32_t *r
   if (!prefix_lens || !qo_indptr || !tree || !q || !out || max_seq_len < 1 ||
       (L.in_full && (!rt || !req_idx)) || (!L.in_full && !plan))
     return fail(c, SWA_ERR_INVALID, "bad attention args");
-  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15)
-    return fail(c, SWA_ERR_INVALID, "q and out must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) |
+       reinterpret_cast<uintptr_t>(tree) | reinterpret_cast<uintptr_t>(plan) |
+       reinterpret_cast<uintptr_t>(ws)) & 15)
+    return fail(c, SWA_ERR_INVALID, "q, out, tree, plan and ws must be 16-byte aligned");
   if (!ws || ws_bytes < swa_attn_tree_ws_bytes(c, layer, bs, n_tokens, max_new, max_seq_len))
     return fail(c, SWA_ERR_INVALID, "split workspace too small");
   const bool tc = use_tree_tc(c, layer);

@@ -25,6 +25,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     k_tree_plan(const int32_t *parents, const int64_t *prefix, const int64_t *qo_indptr,
                 int64_t n_tokens, int max_new, int64_t *positions, TreeView tree, int32_t *err) {
   __shared__ int16_t s_parent[SWA_TREE_MAX_NODES];
+  // The attention launched next may set itself up meanwhile (it waits for this
+  // kernel's end before it reads anything).
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int b = blockIdx.x;
   const int64_t q0 = qo_indptr[b];
   int64_t n = qo_indptr[b + 1] - q0;

@@ -337,13 +337,15 @@ def test_refusals_leave_the_context_usable():
 
     bad = api.SWA_ERR_INVALID
     for kw in (dict(bs=-1), dict(bs=65), dict(n=-1), dict(max_new=0), dict(max_new=1025),
-               dict(parents=None), dict(pre=None), dict(indptr=None), dict(tree=None), dict(nb=8)):
+               dict(parents=None), dict(pre=None), dict(indptr=None), dict(tree=None), dict(nb=8),
+               dict(tree=S.tree.data_ptr() + 4)):
         assert plan(**kw) == bad, kw
     for kw in (dict(layer=2), dict(layer=-1), dict(bs=-1), dict(bs=65), dict(n=-1), dict(max_new=0),
                dict(max_new=1025), dict(msl=0), dict(rt=None), dict(rows=None), dict(pre=None),
                dict(indptr=None), dict(tree=None), dict(q=None), dict(out=None), dict(ws=None),
                dict(nb=16), dict(q=q.data_ptr() + 2), dict(out=out.data_ptr() + 8),
-               dict(layer=0, plan=None)):
+               dict(layer=0, plan=None), dict(tree=S.tree.data_ptr() + 8), dict(layer=0, plan=S.plan.data_ptr() + 4),
+               dict(ws=ws.data_ptr() + 8)):
         assert attn(**kw) == bad, kw
     assert api.swa_tree_bytes(P.ctx, 4, 1025) == 0 and api.swa_tree_bytes(P.ctx, -1, 4) == 0
     assert api.swa_attn_tree_ws_bytes(P.ctx, 5, 2, 4, 4, 100) == 0
