@@ -100,6 +100,7 @@ struct TreeParams {
   int blocks;                // most blocks of 2 T nodes of a request
   int whole;                 // 1: CTAs take whole items, nothing is merged
   int64_t n_tokens;
+  int lookback;              // the plan's
   PlanView plan;
   TreeView tree;
   const float *sinks;
@@ -193,11 +194,15 @@ __device__ __forceinline__ Request request(const TreeParams &P, int b) {
 // its req_to_token entry (full layers) or its page in the request's plan, -1
 // when the plan has none.  An offending page reads as page 0.
 __device__ __forceinline__ int32_t page_rec(bool full, int ps_shift, const int32_t *rt_row,
-                                            const int32_t *hdr, const int32_t *pages, int col) {
+                                            const int32_t *hdr, const int32_t *pages, int first,
+                                            int max_pages, int col) {
   if (full) return rt_row[col];
+  // The plan's first page is known (`first`), so the entry's load does not wait
+  // for the header's, which is checked afterwards.
   const int4 h = *reinterpret_cast<const int4 *>(hdr);   // lo, hi, first page, pages
-  const int k = (col >> ps_shift) - h.z;
-  return (col >= h.x && k >= 0 && k < h.w) ? pages[k] : -1;
+  const int k = (col >> ps_shift) - first;
+  const int32_t page = k >= 0 && k < max_pages ? pages[k] : -1;
+  return (col >= h.x && h.z == first && k < h.w) ? page : -1;
 }
 __device__ __forceinline__ int32_t page_row(const TreeParams &P, bool full, int32_t rec) {
   int64_t page = full ? (rec >= 0 ? rec >> P.ps_shift : -1) : rec;
@@ -269,6 +274,10 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     return;
   }
   if (tid == 0) s_abort = 0;
+  if (tid == 32) {
+    for (const CUtensorMap *m : {&tmK, &tmV, &tmQ})
+      asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+  }
   if (tid < 8) ctl->fills[tid] = 0;
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
@@ -356,7 +365,8 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       return page_rec(full_layer, P.ps_shift,
                       full_layer ? P.rt + P.req_idx[pc.b] * P.rt_stride : nullptr,
                       full_layer ? nullptr : P.plan.hdr + pc.b * 4,
-                      full_layer ? nullptr : P.plan.pages + (int64_t)pc.b * P.plan.max_pages, col);
+                      full_layer ? nullptr : P.plan.pages + (int64_t)pc.b * P.plan.max_pages,
+                      max(pc.prefix - P.lookback, 0) >> P.ps_shift, P.plan.max_pages, col);
     };
     const int n = ring_tiles(sg.mode, sg.n_tiles), n_slots = sg.n_tiles * ppt;
     int32_t rows = page_row(P, full_layer, rec_of(0, 0));   // of batch `cur`
@@ -442,12 +452,11 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     if (P.whole) {
       // The head's line of blocks, every request's the same number of them (some
       // empty), so nothing is summed up; this CTA's stretch of it, 32 at a time.
-      const int per = P.blocks;
-      const int64_t total = (int64_t)P.bs * per, share = (total + P.groups - 1) / P.groups;
-      const int64_t w0 = group_id * share, w1 = min(total, w0 + share);
-      for (int64_t x0 = w0; ok && x0 < w1; x0 += 32) {
-        const int64_t x = x0 + lane;
-        const int b = (int)(x / per), blk = (int)(x % per);
+      const unsigned per = P.blocks, total = P.bs * per, share = (total + P.groups - 1) / P.groups;
+      const unsigned w0 = group_id * share, w1 = min(total, w0 + share);
+      for (unsigned x0 = w0; ok && x0 < w1; x0 += 32) {
+        const unsigned x = x0 + lane;
+        const int b = per == 1 ? x : x / per, blk = x - b * per;
         const Request r = request(P, x < w1 ? b : P.bs);
         Piece mp{b, blk * 2 * T, min(2 * T, r.n - blk * 2 * T), r.q0 + blk * 2 * T, r.col0, r.prefix};
         const int tiles = mp.n_tok > 0 ? block_tiles(P, r, blk) : 0;
@@ -1145,6 +1154,7 @@ cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree,
   P.max_new = a.max_new;
   P.whole = w.whole ? 1 : 0;
   P.n_tokens = a.nq;
+  P.lookback = c.lookback;
   P.plan = a.plan;
   P.tree = tree;
   P.sinks = a.sinks;
