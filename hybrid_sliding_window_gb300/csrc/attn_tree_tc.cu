@@ -320,11 +320,13 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
 
   int q_issued = 0;                          // Q fills, for the abort path
 
-  // Launched as a programmatic dependent: what is above overlaps the kernel
-  // before this one on the stream, everything that reads or writes memory comes
-  // after its completion.
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  // Launched as a programmatic dependent: what comes before each role's call
+  // overlaps the kernel before this one on the stream, everything that reads or
+  // writes global memory comes after that kernel's completion.
+  auto after_previous = [] {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  };
 
   // Warp-collective, warp 10: the Q tiles of the CTA's segment nd, once the last
   // QK^T of the one before has read the buffers.
@@ -417,6 +419,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
   // E4M3 KV: 512 threads x 128 registers = 256 x 152 (softmax) + 256 x 104; whole
   // warpgroups on each side.
   if constexpr (kF8) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;\n");
+  after_previous();
   if (warp == 9) {
     // ===================== producer: segments, K tiles =====================
     int n_pub = 0, base = 0;                 // segments published; ring position
@@ -632,7 +635,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     const uint64_t dq = smem_desc(sb, 16, 1024);
     const uint64_t dk = smem_desc(sb + Gm::kOffRing, 16, 1024);
     const uint64_t dv = smem_desc(sb + Gm::kOffRing, kBlock, 1024);
-    int steps0 = 0, steps1 = 0;              // steps of each group so far
+    int steps0 = 1, steps1 = 1;              // PREADY phases of each group so far (the first: warm-up)
     int base = 0;                            // ring position of the segment's first tile
     for (int nd = 0;; ++nd) {
       const int slot = nd & 1;
@@ -644,6 +647,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       const int U = mode == kAlternate ? tiles : 2 * tiles, n = ring_tiles(mode, tiles);
       const bool shared = mode == kShared;   // a K/V tile serves two steps
       if (!wait_all(bar(kF8 ? B_QCONV : B_FULLQ), nd & 1)) break;
+      if (nd == 0 && !(wait_all(bar(B_PREADY), 0) && wait_all(bar(B_PREADY + 1), 0))) break;
       int ok = 1;
       if (elect_one()) {
         for (int u = -2; u < U; ++u) {       // u = -2, -1: S(0) and S(1) only
@@ -695,7 +699,6 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     const uint32_t tS = tmem + grp * 128 + lane_off;
     const uint32_t tO = tmem + 256 + grp * kD + lane_off;
     const int head = kvh * G + r % G;
-    const float sg2 = P.sinks && r < TG ? P.sinks[head] * 1.4426950408889634f : -INFINITY;
     const float sc = P.scale_log2;
     const uint64_t sc2 = f2pack(sc, sc);
     int steps = 0, joins = 0;
@@ -729,9 +732,14 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       __syncwarp();
       return true;
     };
-    Mine next;
-    for (int nd = 0;; ++nd) {
-      if (nd == 0 && !take(0, next)) break;
+    // Turn -1 runs the tile loop on whatever the tensor memory holds, for the
+    // instruction cache: cold, a CTA's first tile took 6400 cycles instead of
+    // 2700, and these warps have nothing to do until the first S is there.  Its
+    // PREADY lets the first S in.
+    Mine next{kShared, 1, -1, 0, 0, Piece{0, 0, 0, 0, 0, 32}, false, 0ull};
+    float sg2 = -INFINITY;
+    for (int nd = -1;; ++nd) {
+      const bool warming = nd < 0;
       const Mine cur = next;
       if (cur.mode < 0) break;
       const int mode = cur.mode, n_tiles = cur.n_tiles, tr = cur.tr, part_slot = cur.part;
@@ -739,7 +747,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       const bool alone = mode != kAlternate;           // this group's rows are its own
       const bool row_valid = cur.valid;
       const uint64_t above = cur.above;
-      const bool any_row = __any_sync(0xffffffffu, row_valid);
+      const bool any_row = warming || __any_sync(0xffffffffu, row_valid);
       const uint32_t *row = P.tree.mask + (int64_t)(pc.q0 + (row_valid ? tr : 0)) * P.tree.words;
       // Relative to the piece's first column: the row's first column, and the
       // first behind the cached ones.
@@ -749,21 +757,23 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
         lo_row = (int)tree_first_col(first_position(P.kind, P.window, pc.prefix + cur.depth),
                                      pc.prefix, pc.n0 + tr, cur.depth, row) -
                  pc.col0;
-      float m_run = row_valid ? -INFINITY : 0.f, l_run = 0.f;
+      float m_run = row_valid || warming ? -INFINITY : 0.f, l_run = 0.f;
       bool alive = true, first = true;
       for (int t = alone ? 0 : grp; t < n_tiles; t += alone ? 1 : 2) {
-        if (!wait_all(bar(B_SDONE + grp), steps & 1)) {
-          alive = false;
-          break;
+        if (!warming) {
+          if (!wait_all(bar(B_SDONE + grp), steps & 1)) {
+            alive = false;
+            break;
+          }
+          ++steps;
         }
-        ++steps;
         tc_fence_after();
         uint64_t acc2[2] = {0ull, 0ull};
 #pragma unroll 1
         for (int cb = 0; any_row && cb < 2; ++cb) {
           const int c0 = t * kKeys + cb * 64;        // the chunk's first column
           // Columns of the chunk this row reads.
-          const bool edge = row_valid && !(c0 >= lo_row && c0 + 64 <= behind);
+          const bool edge = warming || (row_valid && !(c0 >= lo_row && c0 + 64 <= behind));
           uint64_t allow = row_valid ? ~0ull : 0ull;
           const bool any_edge = __any_sync(0xffffffffu, edge);
           if (any_edge) {
@@ -885,7 +895,12 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
         tc_fence_before();
         mbar_arrive(bar(B_PREADY + grp));
       }
+      if (warming) {
+        after_previous();
+        if (P.sinks && r < TG) sg2 = P.sinks[head] * 1.4426950408889634f;
+      }
       if (!alive || !take(nd + 1, next)) break;
+      if (warming) continue;
       // ---- epilogue ----
       if (!wait_all(bar(B_ODONE + grp), nd & 1)) break;
       float w0 = 1.f, w1 = 0.f;              // weights of this group's and the other's O
