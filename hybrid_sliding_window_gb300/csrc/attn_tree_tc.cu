@@ -759,6 +759,11 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
                  pc.col0;
       float m_run = row_valid || warming ? -INFINITY : 0.f, l_run = 0.f;
       bool alive = true, first = true;
+      // Uniform over the warp: no row's columns begin after `lo_most`, and every
+      // row has a reference maximum (`settled`); interior chunks then need no vote
+      // before their exponentials.
+      const int lo_most = __reduce_max_sync(0xffffffffu, row_valid ? lo_row : -0x7fffffff);
+      bool settled = false;
       for (int t = alone ? 0 : grp; t < n_tiles; t += alone ? 1 : 2) {
         if (!warming) {
           if (!wait_all(bar(B_SDONE + grp), steps & 1)) {
@@ -773,11 +778,10 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
         for (int cb = 0; any_row && cb < 2; ++cb) {
           const int c0 = t * kKeys + cb * 64;        // the chunk's first column
           // Columns of the chunk this row reads.
-          const bool edge = warming || (row_valid && !(c0 >= lo_row && c0 + 64 <= behind));
           uint64_t allow = row_valid ? ~0ull : 0ull;
-          const bool any_edge = __any_sync(0xffffffffu, edge);
+          const bool any_edge = warming || c0 < lo_most || c0 + 64 > behind;
           if (any_edge) {
-            if (edge) {
+            if (row_valid || warming) {
               allow = bit_range(lo_row - c0, behind - c0);
               if (c0 + 64 > behind)
                 allow |= (few ? shift_bits(above, c0 - behind)
@@ -808,7 +812,11 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
           // chunk's own maximum is computed only for a row's first chunk and
           // when the weights' sum shows that a score outgrew the reference.
           // Raising the reference rescales what was summed against the old one.
-          bool redo = __any_sync(0xffffffffu, m_run == -INFINITY);
+          bool redo = false;
+          if (!settled) {
+            redo = __any_sync(0xffffffffu, m_run == -INFINITY);
+            settled = !redo;
+          }
           uint32_t pk[32];
           uint64_t c2[2];
 #pragma unroll 1
