@@ -56,7 +56,6 @@
 
 #include <math.h>
 
-#include <type_traits>
 
 #include "spec_internal.h"
 #include "tc_ptx.cuh"
@@ -73,8 +72,8 @@ constexpr int kTreeThreads = 384;            // 8 softmax warps, MMA, and three 
 constexpr int kConvThreads = 128;            // E4M3 KV: warps 12-15 convert
 constexpr float kRescaleGap = 8.f;           // log2 units: rescale O when the max grows more
 constexpr float kSumCap = 32768.f;           // a chunk's weight sum that forces a maximum pass
-constexpr int kMergeThreads = 128;
-constexpr int kMergeRows = 16;               // rows of one merge CTA
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = 32;               // rows of one merge CTA: one per lane
 
 template <int D, bool F8>
 struct TreeGeo {
@@ -107,7 +106,8 @@ struct TreeParams {
   float scale_log2;          // E4M3 KV: with the K scale
   float v_scale;             // 1 unless E4M3 KV
   __nv_bfloat16 *out;
-  float *partials;           // [CTA][2][rows x D, then rows x 2]
+  float *partials;           // [CTA][2][D / 4][rows][4], then [rows][2] (max, sum)
+  int rows_max;              // rows of an item
   int64_t part_stride;       // floats of one partial
   struct MergeDesc *desc;    // [CTA]
   int32_t *err;
@@ -940,9 +940,8 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       const int row_i = (mode == kShared ? grp * TG : 0) + r;      // row of the item
       float *part = part_slot < 0 ? nullptr
                                 : P.partials + ((int64_t)blockIdx.x * 2 + part_slot) * P.part_stride;
-      const int rows_max = (int)(P.part_stride / (kD + 2));
       if (part && row_valid && (alone || grp == 0))
-        reinterpret_cast<float2 *>(part + (int64_t)rows_max * kD)[row_i] = make_float2(m_run, l_run);
+        reinterpret_cast<float2 *>(part + P.rows_max * kD)[row_i] = make_float2(m_run, l_run);
       __nv_bfloat16 *orow = P.out + ((int64_t)(pc.q0 + tr) * (P.hkv * G) + head) * kD;
       const int d_lo = alone ? 0 : grp * (kD / 2), d_hi = alone ? kD : d_lo + kD / 2;
       const uint32_t tO2 = tmem + 256 + (grp ^ 1) * kD + lane_off;
@@ -967,10 +966,11 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
           }
         }
         if (part && row_valid) {
-          float4 *dst = reinterpret_cast<float4 *>(part + (int64_t)row_i * kD + d);
+          // Four dims of all rows together: a warp's rows are neighbours.
+          float4 *dst = reinterpret_cast<float4 *>(part) + (d / 4) * P.rows_max + row_i;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(__uint_as_float(a[4 * e]), __uint_as_float(a[4 * e + 1]),
+            dst[e * P.rows_max] = make_float4(__uint_as_float(a[4 * e]), __uint_as_float(a[4 * e + 1]),
                                  __uint_as_float(a[4 * e + 2]), __uint_as_float(a[4 * e + 3]));
         } else if (row_valid) {
 #pragma unroll
@@ -1019,67 +1019,57 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
 }
 
 // Merges the partials of the items that cross CTAs: CTA (chunk, c) the rows
-// [16 chunk, 16 chunk + 16) of the item that CTA c of the main launch began and
-// left.  A warp takes a row: the contributors' maxima and sums first, then the
-// weighted sum of their output rows, in group order.
+// [32 chunk, 32 chunk + 32) of the item that CTA c of the main launch began and
+// left, in group order.  A lane has a row and a warp D / 8 of its dims, so that
+// partials are read as they were written, whole lines at a time.
 template <int kD>
 __global__ void __launch_bounds__(kMergeThreads) k_tree_merge(const __grid_constant__ TreeParams P) {
-  constexpr int kPer = kD / 32;              // floats per lane
-  using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
+  constexpr int kQuads = kD / 4 / (kMergeThreads / 32);   // float4s of a lane
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const MergeDesc d = P.desc[blockIdx.y];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q0 = (threadIdx.x >> 5) * kQuads, r = blockIdx.x * kMergeRows + (threadIdx.x & 31);
   const int kvh = blockIdx.y % P.hkv, G = P.G;
-  const int rows_max = (int)(P.part_stride / (kD + 2));
+  if (d.parts < 2 || r >= d.n_tok * G) return;
+  const int head = kvh * G + r % G;
   auto part = [&](int i) {
     return P.partials +
            (((int64_t)blockIdx.y + (int64_t)i * P.hkv) * 2 + (i == 0 ? 1 : 0)) * P.part_stride;
   };
-  if (d.parts < 2) return;
-  for (int i = warp; i < kMergeRows; i += kMergeThreads / 32) {
-    const int r = blockIdx.x * kMergeRows + i;
-    if (r >= d.n_tok * G) break;
-    const int head = kvh * G + r % G;
-    auto stat = [&](int k) {
-      return reinterpret_cast<const float2 *>(part(k) + (int64_t)rows_max * kD)[r];
-    };
-    float mx = -INFINITY;
-    for (int k = lane; k < d.parts; k += 32) mx = fmaxf(mx, stat(k).x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float sg2 = P.sinks ? P.sinks[head] * 1.4426950408889634f : -INFINITY;
-    const float M = fmaxf(mx, sg2);
-    float L = 0.f, acc[kPer];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-    for (int k0 = 0; k0 < d.parts; k0 += 32) {
-      float w = 0.f;
-      if (k0 + lane < d.parts) {
-        const float2 s = stat(k0 + lane);
-        w = s.x == -INFINITY ? 0.f : exp2f(s.x - M);
-        L += w * s.y;
-      }
-      const int m = min(32, d.parts - k0);
+  auto stat = [&](int i) {
+    return reinterpret_cast<const float2 *>(part(i) + P.rows_max * kD)[r];
+  };
+  const float sg2 = P.sinks ? P.sinks[head] * 1.4426950408889634f : -INFINITY;
+  float M = sg2;
 #pragma unroll 4
-      for (int k = 0; k < m; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const Vec v = *reinterpret_cast<const Vec *>(part(k0 + k) + (int64_t)r * kD + lane * kPer);
-        const float *x = reinterpret_cast<const float *>(&v);
+  for (int i = 0; i < d.parts; ++i) M = fmaxf(M, stat(i).x);
+  float L = P.sinks ? exp2f(sg2 - M) : 0.f;
+  float4 acc[kQuads];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = wk != 0.f ? fmaf(x[e], wk, acc[e]) : acc[e];
-      }
+  for (int e = 0; e < kQuads; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < d.parts; ++i) {
+    const float2 s = stat(i);
+    const float w = s.x == -INFINITY ? 0.f : exp2f(s.x - M);
+    L += w * s.y;
+    const float4 *src = reinterpret_cast<const float4 *>(part(i)) + q0 * P.rows_max + r;
+#pragma unroll
+    for (int e = 0; e < kQuads; ++e) {
+      const float4 v = src[e * P.rows_max];
+      acc[e].x = fmaf(v.x, w, acc[e].x);
+      acc[e].y = fmaf(v.y, w, acc[e].y);
+      acc[e].z = fmaf(v.z, w, acc[e].z);
+      acc[e].w = fmaf(v.w, w, acc[e].w);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (P.sinks) L += exp2f(sg2 - M);
-    const float f = P.v_scale / L;
-    __nv_bfloat16 *dst =
-        P.out + ((int64_t)(d.q0 + r / G) * (P.hkv * G) + head) * kD + lane * kPer;
-#pragma unroll
-    for (int e = 0; e < kPer; e += 2)
-      *reinterpret_cast<uint32_t *>(dst + e) = pack_p<false>(acc[e] * f, acc[e + 1] * f);
   }
+  const float f = P.v_scale / L;
+  __nv_bfloat16 *dst = P.out + ((int64_t)(d.q0 + r / G) * (P.hkv * G) + head) * kD + q0 * 4;
+#pragma unroll
+  for (int e = 0; e < kQuads; e += 2)
+    *reinterpret_cast<uint4 *>(dst + 4 * e) =
+        make_uint4(pack_p<false>(acc[e].x * f, acc[e].y * f), pack_p<false>(acc[e].z * f, acc[e].w * f),
+                   pack_p<false>(acc[e + 1].x * f, acc[e + 1].y * f),
+                   pack_p<false>(acc[e + 1].z * f, acc[e + 1].w * f));
 }
 
 int tile_nodes(const Ctx &c, int layer, int max_new) {
@@ -1100,9 +1090,9 @@ TreeWs tree_ws(const Ctx &c, int layer, int max_new, int max_seq_len) {
   w.groups = std::max(1, (c.num_sms > 0 ? c.num_sms : 148) / L.hkv);
   w.rows = std::min(2 * T, max_new) * G;
   w.whole = tree_max_keys(c, layer, max_new, max_seq_len) <= 512;
+  // whole 128-byte lines of four dims x 32 rows
+  w.rows = (w.rows + 31) / 32 * 32;
   w.part_stride = (int64_t)w.rows * (c.cfg.head_dim + 2);
-  // the statistics are read as pairs, the next partial's rows as 16-byte words
-  w.part_stride = (w.part_stride + 3) / 4 * 4;
   w.desc_bytes = ((size_t)w.groups * L.hkv * sizeof(MergeDesc) + 255) / 256 * 256;
   w.total = w.whole ? 256
                     : w.desc_bytes + (size_t)w.groups * L.hkv * 2 * w.part_stride * sizeof(float);
@@ -1188,6 +1178,7 @@ cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree,
   P.desc = static_cast<MergeDesc *>(a.ws);
   P.partials = reinterpret_cast<float *>(static_cast<char *>(a.ws) + w.desc_bytes);
   P.part_stride = w.part_stride;
+  P.rows_max = w.rows;
   P.err = c.err_word;
   CUtensorMap tmq;
   if (!make_q_tile_map(&tmq, a.q, a.nq, c.cfg.num_q_heads, c.cfg.head_dim, P.G, P.T))
