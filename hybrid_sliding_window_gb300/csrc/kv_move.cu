@@ -5,10 +5,13 @@
 // A token's row is Hkv x D elements at its full slot on full layers and at
 // full_to_swa[slot] on the others ("SWA in SGLang" design note, "two pools and
 // the mapping"), K and V of every layer.  The moves are pure copies, bound by
-// HBM: bytes read + bytes written.  A warp owns one 512-byte column of one
-// layer's K or V row (32 lanes x 16 bytes, coalesced both ways), looks the
-// slots of up to 32 moves up with its lanes in one go, and keeps the loads of
-// kAhead rows in flight before it stores any.
+// HBM: bytes read + bytes written.  A warp moves 512 bytes at a time (32 lanes x
+// 16 bytes, coalesced both ways), looks the slots of up to 32 moves up with its
+// lanes in one go, and keeps kAhead loads in flight before it stores any.  A copy
+// of many rows gives a warp one 512-byte column of one layer's K or V rows; a
+// commit has few rows per request, so there a warp takes whole K and V rows of a
+// layer and the chain of lookups (length, row, two slots, two mappings) is paid
+// once for all of them (64 requests, 48 layers, 65 MB: 15.1 -> 10.6 us).
 #include <cuda_runtime.h>
 
 #include "spec_internal.h"
@@ -117,32 +120,64 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
   run_moves((blockIdx.y & 1) ? L.v : L.k, col, col < L.row_bytes, live, ra, rb);
 }
 
-// grid: x = requests x 512-byte columns, y = 2 x layer + (K or V).  Node
-// accepted[j] >= j moves to column prefix + j.  Ascending order makes the
-// moves safe in place: a move writes a column below every later source, and
-// its own source is only overwritten by a later move - whose stores follow
-// this warp's loads of the earlier moves (batches go in order; within a batch
-// loads precede stores), and no other warp touches these bytes.
+// The same for whole K and V rows: 2 x cols columns per move, in move order, so
+// that every column sees its moves in lane order.
+__device__ __forceinline__ void run_row_moves(char *k, char *v, int row_bytes, int lane, bool live,
+                                              int64_t ra, int64_t rb) {
+  const int cols = (row_bytes + 511) / 512;
+  unsigned todo = __ballot_sync(0xffffffffu, live);
+  int l = todo ? __ffs(todo) - 1 : 0, seg = 0;   // move, column of it (K's, then V's)
+  while (todo) {
+    uint4 x[kAhead];
+    char *to[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      to[u] = nullptr;
+      if (todo) {
+        const int c = seg < cols ? seg : seg - cols;
+        char *base = (seg < cols ? k : v) + c * 512 + lane * 16;
+        const int64_t from = __shfl_sync(0xffffffffu, ra, l), dst = __shfl_sync(0xffffffffu, rb, l);
+        if (c * 512 + lane * 16 < row_bytes) {
+          x[u] = *reinterpret_cast<const uint4 *>(base + from);
+          to[u] = base + dst;
+        }
+        if (++seg == 2 * cols) {
+          seg = 0;
+          todo &= todo - 1;
+          l = todo ? __ffs(todo) - 1 : 0;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (to[u]) *reinterpret_cast<uint4 *>(to[u]) = x[u];
+  }
+}
+
+// grid: x = requests, y = layer.  Node accepted[j] >= j moves to column prefix +
+// j.  Ascending order makes the moves safe in place: a move writes a column
+// below every later source, and its own source is only overwritten by a later
+// move - whose stores follow this warp's loads of the earlier moves (batches go
+// in order; within a batch loads precede stores), and no other warp touches
+// these bytes.
 __global__ void __launch_bounds__(kMoveWarps * 32)
-    k_commit_tree(const __grid_constant__ MoveParams P, int bs, int cols) {
+    k_commit_tree(const __grid_constant__ MoveParams P, int bs) {
   const int lane = threadIdx.x & 31;
-  const int64_t w = blockIdx.x * (int64_t)kMoveWarps + (threadIdx.x >> 5);
-  const int64_t b = w / cols;
-  const MoveLayer &L = P.layer[blockIdx.y >> 1];
-  const int64_t col = (w % cols) * 512 + lane * 16;
-  if (b >= bs || (w % cols) * 512 >= L.row_bytes) return;
-  char *base = (blockIdx.y & 1) ? L.v : L.k;
+  const int b = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
+  const MoveLayer &L = P.layer[blockIdx.y];
+  if (b >= bs) return;
   const int64_t pre = P.prefix[b];
-  int n = P.n_accepted[b];
+  const int32_t *row = P.rt + P.req_idx[b] * P.rt_stride;
+  int a = lane < P.max_accept ? P.accepted[(int64_t)b * P.max_accept + lane] : 0;
+  const int n = P.n_accepted[b];
   if (n < 0 || n > P.max_accept || pre < 0) {
     set_error(P.err, SWA_DEVERR_RANGE);
     return;
   }
-  const int32_t *row = P.rt + P.req_idx[b] * P.rt_stride;
   int prev = -1;
   for (int j0 = 0; j0 < n; j0 += 32) {
     const int j = j0 + lane;
-    const int a = j < n ? P.accepted[b * P.max_accept + j] : 0;
+    if (j0 > 0) a = j < n ? P.accepted[(int64_t)b * P.max_accept + j] : 0;
     int before = __shfl_up_sync(0xffffffffu, a, 1);
     if (lane == 0) before = prev;
     prev = __shfl_sync(0xffffffffu, a, 31);
@@ -153,7 +188,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
     int64_t ra = 0, rb = 0;
     bool live = j < n && (!wrong || lane < __ffs(wrong) - 1) && a != j;
     if (live) live = move_rows(P, L, row[pre + a], row[pre + j], ra, rb);
-    run_moves(base, col, col < L.row_bytes, live, ra, rb);
+    run_row_moves(L.k, L.v, L.row_bytes, lane, live, ra, rb);
     if (wrong) {
       set_error(P.err, SWA_DEVERR_RANGE);
       return;
@@ -217,10 +252,9 @@ cudaError_t launch_commit_tree(Ctx &c, int bs, const int32_t *rt, int64_t rt_str
   P.accepted = accepted;
   P.n_accepted = n_accepted;
   P.max_accept = max_accept;
-  return for_layers(c, P, [&](const MoveParams &p, int nl, int cols) {
-    const int64_t warps = (int64_t)bs * cols;
-    dim3 grid((unsigned)((warps + kMoveWarps - 1) / kMoveWarps), 2 * nl);
-    k_commit_tree<<<grid, kMoveWarps * 32, 0, s>>>(p, bs, cols);
+  return for_layers(c, P, [&](const MoveParams &p, int nl, int) {
+    dim3 grid((bs + kMoveWarps - 1) / kMoveWarps, nl);
+    k_commit_tree<<<grid, kMoveWarps * 32, 0, s>>>(p, bs);
   });
 }
 
