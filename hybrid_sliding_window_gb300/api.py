@@ -572,9 +572,9 @@ def _rows_ptr(t):
     if t is None:
         return None, 0
     assert t.is_cuda, "device buffer expected"
-    assert t.dim() == 3 and t.stride(2) == 1 and t.stride(1) == t.shape[2], \
-        "heads of a token must be contiguous"
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    (n, heads, dim), (token, head, one) = t.shape, t.stride()
+    assert one == 1 and head == dim, "heads of a token must be contiguous"
+    return t.data_ptr(), token if n > 1 else heads * dim
 
 
 def swa_qk_norm_rope_store(ctx, layer, q, k, v, positions, full_loc, q_out, swa_loc=None,

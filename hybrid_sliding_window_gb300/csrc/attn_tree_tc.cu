@@ -1101,13 +1101,13 @@ TreeWs tree_ws(const Ctx &c, int layer, int max_new, int max_seq_len) {
 
 template <int D, bool F8>
 cudaError_t launch_tree(const LayerInfo &L, const CUtensorMap &tmq, const TreeParams &P, int rows,
-                        cudaStream_t s) {
+                        int device, cudaStream_t s) {
   using Gm = TreeGeo<D, F8>;
   const size_t smem = Gm::kOffCtl + sizeof(Control);
   static_assert(B_COUNT == 40 && Gm::kOffCtl + sizeof(Control) <= 227 * 1024,
                 "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(k_tree_tc<D, F8>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(k_tree_tc<D, F8>, smem, device, done);
   if (e != cudaSuccess) return e;
   const int ctas = P.groups * P.hkv;
   cudaLaunchAttribute attr;
@@ -1183,9 +1183,9 @@ cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree,
   CUtensorMap tmq;
   if (!make_q_tile_map(&tmq, a.q, a.nq, c.cfg.num_q_heads, c.cfg.head_dim, P.G, P.T))
     return cudaErrorInvalidValue;
-  if (f8) return launch_tree<128, true>(L, tmq, P, w.rows, s);
-  return c.cfg.head_dim == 64 ? launch_tree<64, false>(L, tmq, P, w.rows, s)
-                              : launch_tree<128, false>(L, tmq, P, w.rows, s);
+  if (f8) return launch_tree<128, true>(L, tmq, P, w.rows, c.device, s);
+  return c.cfg.head_dim == 64 ? launch_tree<64, false>(L, tmq, P, w.rows, c.device, s)
+                              : launch_tree<128, false>(L, tmq, P, w.rows, c.device, s);
 }
 
 }  // namespace swa

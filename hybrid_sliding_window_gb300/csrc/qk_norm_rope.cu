@@ -430,8 +430,8 @@ cudaError_t launch_one(const Ctx &c, NormParams P, int64_t n, cudaStream_t s) {
   P.chunks = (rows + P.chunk_rows - 1) / P.chunk_rows;
   P.chunk_rows = (rows + P.chunks - 1) / P.chunks;
   P.units = n * P.chunks;
-  cudaError_t e = cudaFuncSetAttribute(k_qk_norm_rope_store<T, D, kF8, kInter>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(k_qk_norm_rope_store<T, D, kF8, kInter>, kSmem, c.device, done);
   if (e != cudaSuccess) return e;
   const int64_t grid = P.units < ctas ? P.units : ctas;
   P.step_t = (int)(grid / P.chunks);

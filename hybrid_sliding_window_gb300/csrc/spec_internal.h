@@ -2,6 +2,8 @@
 // and tree attention, the q/k norm + rotation + store, and the row moves.
 #pragma once
 
+#include <atomic>
+
 #include "swa_internal.h"
 
 namespace swa {
@@ -55,6 +57,18 @@ __host__ __device__ inline int64_t first_position(int kind, int window, int64_t 
   if (kind == SWA_LAYER_FULL) return 0;
   if (kind == SWA_LAYER_SLIDING) return p - window > 0 ? p - window : 0;
   return (p / window) * window;
+}
+
+// Raises a kernel's dynamic shared memory limit, once per device and kernel
+// (`done`: one bit per device; a repeated call is harmless).
+template <typename K>
+cudaError_t allow_smem(K *kernel, size_t bytes, int device, std::atomic<uint64_t> &done) {
+  const uint64_t bit = 1ull << (device & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && device < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // ---- tree_plan.cu -----------------------------------------------------------
