@@ -98,6 +98,7 @@ struct TreeParams {
   int bs, groups, max_new;
   int blocks;                // most blocks of 2 T nodes of a request
   int whole;                 // 1: CTAs take whole items, nothing is merged
+  int wide_out;              // out is 32-byte aligned
   int64_t n_tokens;
   int lookback;              // the plan's
   PlanView plan;
@@ -371,9 +372,9 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
                       max(pc.prefix - P.lookback, 0) >> P.ps_shift, P.plan.max_pages, col);
     };
     const int n = ring_tiles(sg.mode, sg.n_tiles), n_slots = sg.n_tiles * ppt;
-    int32_t rows = page_row(P, full_layer, rec_of(0, 0));   // of batch `cur`
-    int32_t rows_two = rows;                                // a pair's second piece
-    if (pair) rows_two = page_row(P, full_layer, rec_of(1, 0));
+    const int32_t rec0 = rec_of(0, 0), rec1 = pair ? rec_of(1, 0) : 0;
+    int32_t rows = page_row(P, full_layer, rec0);           // of batch `cur`
+    const int32_t rows_two = pair ? page_row(P, full_layer, rec1) : 0;   // a pair's second piece
     int32_t rec_next = !pair && n_slots > 32 ? rec_of(0, 1) : 0;
     int cur = 0;
     auto load_tile = [&](int x, int pos, const CUtensorMap *map) {
@@ -973,14 +974,25 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
             dst[e * P.rows_max] = make_float4(__uint_as_float(a[4 * e]), __uint_as_float(a[4 * e + 1]),
                                  __uint_as_float(a[4 * e + 2]), __uint_as_float(a[4 * e + 3]));
         } else if (row_valid) {
+          // Every lane has a row of its own, so a store costs the load-store unit
+          // a cycle per lane: 32 bytes at a time where the output allows it.
+          uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
+          for (int k = 0; k < 16; ++k)
+            w[k] = pack_p<false>(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1]));
+          if (P.wide_out) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack_p<false>(__uint_as_float(a[8 * e + 2 * k]),
-                                   __uint_as_float(a[8 * e + 2 * k + 1]));
-            *reinterpret_cast<uint4 *>(orow + d + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < 16; k += 8)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(
+                               orow + d + 2 * k),
+                           "r"(w[k]), "r"(w[k + 1]), "r"(w[k + 2]), "r"(w[k + 3]), "r"(w[k + 4]),
+                           "r"(w[k + 5]), "r"(w[k + 6]), "r"(w[k + 7])
+                           : "memory");
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<uint4 *>(orow + d + 2 * k) =
+                  make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
           }
         }
         __syncwarp();   // the TMEM loads are warp-collective
@@ -1175,6 +1187,7 @@ cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree,
   P.scale_log2 = a.scale * 1.4426950408889634f * (f8 ? a.k_scale : 1.f);
   P.v_scale = f8 ? a.v_scale : 1.f;
   P.out = static_cast<__nv_bfloat16 *>(a.out);
+  P.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 ? 1 : 0;
   P.desc = static_cast<MergeDesc *>(a.ws);
   P.partials = reinterpret_cast<float *>(static_cast<char *>(a.ws) + w.desc_bytes);
   P.part_stride = w.part_stride;

@@ -217,6 +217,36 @@ def test_wide_scores(shape, path):
     assert api.swa_device_check(P.ctx) == 0
 
 
+@pytest.mark.parametrize("shape", [MIMO, GPTOSS, LLAMA4], ids=["mimo", "gptoss", "llama4"])
+def test_long_windows(shape):
+    """Windows of more keys than a work item keeps whole: split and merged like
+    full layers, with a first column inside a page, and nodes on both sides of a
+    chunk's border."""
+    hkv = shape["layers"][1][2]
+    layers = [(OT.SLIDING, 1000, hkv), (OT.CHUNKED, 1500, hkv), (OT.SLIDING, 600, hkv)]
+    rng = np.random.default_rng(18)
+    parents = [random_parents(rng, 33), list(range(-1, 29)), random_parents(rng, 9)]
+    P, S = _step(shape, 16, [4483, 1490, 20], parents, layers=layers)
+    for l in range(3):
+        S.check(l, what="long window")
+    assert api.swa_device_check(P.ctx) == 0
+
+
+def test_output_alignment():
+    """An output that is 16-byte but not 32-byte aligned gets the same bits."""
+    for shape, prompt in ((MIMO, [700, 65]), (GPTOSS, [700, 65]), (LLAMA4, [100, 20])):
+        P, S = _step(shape, 64, prompt, _trees(19, [9, 12]))
+        for l in range(2):
+            q = P.to_dev(S.queries(l))
+            out = torch.empty_like(q)
+            S.run(l, q, out, S.workspace(l))
+            buf = torch.full((q.numel() + 16,), 3.0, dtype=q.dtype, device="cuda")
+            off = buf[8:8 + q.numel()].view(q.shape)
+            assert off.data_ptr() % 32 == 16
+            S.run(l, q, off, S.workspace(l))
+            assert torch.equal(off, out) and (buf[:8] == 3).all() and (buf[8 + q.numel():] == 3).all()
+
+
 def test_chain_equals_extend():
     """A chain is the causal chunk that swa_attn_extend attends."""
     P, S = _step(MIMO, 64, [700, 333], [list(range(-1, 39)), list(range(-1, 6))])
