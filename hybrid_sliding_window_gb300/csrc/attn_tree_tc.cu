@@ -1092,10 +1092,13 @@ struct TreeWs {
   int groups, rows;          // CTAs per KV head; rows of an item
   bool whole;                // items are not split
   int64_t part_stride;       // floats
-  size_t desc_bytes, total;
+  size_t desc_off, part_off, total;
 };
 
-TreeWs tree_ws(const Ctx &c, int layer, int max_new, int max_seq_len) {
+// [reserved][tickets] as in the other attention families, which this one leaves
+// untouched (so calls of either may share a workspace), then the descriptors and
+// partials.
+TreeWs tree_ws(const Ctx &c, int layer, int64_t nq, int max_new, int max_seq_len) {
   const LayerInfo &L = c.layers[layer];
   TreeWs w;
   const int G = c.cfg.num_q_heads / L.hkv, T = tile_nodes(c, layer, max_new);
@@ -1105,9 +1108,10 @@ TreeWs tree_ws(const Ctx &c, int layer, int max_new, int max_seq_len) {
   // whole 128-byte lines of four dims x 32 rows
   w.rows = (w.rows + 31) / 32 * 32;
   w.part_stride = (int64_t)w.rows * (c.cfg.head_dim + 2);
-  w.desc_bytes = ((size_t)w.groups * L.hkv * sizeof(MergeDesc) + 255) / 256 * 256;
-  w.total = w.whole ? 256
-                    : w.desc_bytes + (size_t)w.groups * L.hkv * 2 * w.part_stride * sizeof(float);
+  w.desc_off = ws_partials_off(c, nq);
+  const size_t ctas = (size_t)w.groups * L.hkv;
+  w.part_off = w.desc_off + (ctas * sizeof(MergeDesc) + 255) / 256 * 256;
+  w.total = w.whole ? w.desc_off : w.part_off + ctas * 2 * w.part_stride * sizeof(float);
   return w;
 }
 
@@ -1150,14 +1154,14 @@ bool tc_tree_supported(const Ctx &c, int layer) {
           (c.cfg.kv_dtype == SWA_DTYPE_E4M3 && d == 128));
 }
 
-size_t tc_tree_ws_bytes(const Ctx &c, int layer, int max_new, int max_seq_len) {
-  return (tree_ws(c, layer, max_new, max_seq_len).total + 255) / 256 * 256;
+size_t tc_tree_ws_bytes(const Ctx &c, int layer, int64_t nq, int max_new, int max_seq_len) {
+  return (tree_ws(c, layer, nq, max_new, max_seq_len).total + 255) / 256 * 256;
 }
 
 cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree, cudaStream_t s) {
   if (a.nq == 0) return cudaSuccess;
   const LayerInfo &L = c.layers[a.layer];
-  const TreeWs w = tree_ws(c, a.layer, a.max_new, a.max_seq_len);
+  const TreeWs w = tree_ws(c, a.layer, a.nq, a.max_new, a.max_seq_len);
   TreeParams P{};
   P.kind = L.kind;
   P.window = L.window;
@@ -1188,8 +1192,9 @@ cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree,
   P.v_scale = f8 ? a.v_scale : 1.f;
   P.out = static_cast<__nv_bfloat16 *>(a.out);
   P.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 ? 1 : 0;
-  P.desc = static_cast<MergeDesc *>(a.ws);
-  P.partials = reinterpret_cast<float *>(static_cast<char *>(a.ws) + w.desc_bytes);
+  char *ws = static_cast<char *>(a.ws);
+  P.desc = reinterpret_cast<MergeDesc *>(ws + w.desc_off);
+  P.partials = reinterpret_cast<float *>(ws + w.part_off);
   P.part_stride = w.part_stride;
   P.rows_max = w.rows;
   P.err = c.err_word;

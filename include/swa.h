@@ -652,8 +652,8 @@ swa_status swa_tree_plan(swa_ctx *ctx, int32_t bs, const int32_t *parents,
  * prefix_lens, seq = prefix + nodes and the same max_new; max_seq_len bounds
  * seq.  q, out: [n_tokens][Hq][D], f32 for an F32 pool, bf16 otherwise; q, out,
  * tree, plan and ws are 16-byte aligned.  Rows of entries that belong to no request are left as they are.
- * `ws` as for swa_attn_decode (zero before its first use, reusable; calls that
- * may overlap on the GPU need their own). */
+ * `ws` as for swa_attn_decode (zero before its first use, reusable, also by
+ * swa_attn_decode; calls that may overlap on the GPU need their own). */
 size_t swa_attn_tree_ws_bytes(const swa_ctx *ctx, int32_t layer, int32_t bs,
                               int64_t n_tokens, int32_t max_new,
                               int32_t max_seq_len);

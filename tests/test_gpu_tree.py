@@ -225,7 +225,7 @@ def test_long_windows(shape):
     hkv = shape["layers"][1][2]
     layers = [(OT.SLIDING, 1000, hkv), (OT.CHUNKED, 1500, hkv), (OT.SLIDING, 600, hkv)]
     rng = np.random.default_rng(18)
-    parents = [random_parents(rng, 33), list(range(-1, 29)), random_parents(rng, 9)]
+    parents = [random_parents(rng, 14), list(range(-1, 14)), random_parents(rng, 5)]
     P, S = _step(shape, 16, [4483, 1490, 20], parents, layers=layers)
     for l in range(3):
         S.check(l, what="long window")
@@ -338,6 +338,41 @@ def test_repeats_streams_and_graphs():
         q = S.queries(l)
         at, ref, mag = S.oracle(l, q)
         assert_attention(outs[l].float().cpu().numpy()[at], ref, mag, "bf16", "stars")
+    assert api.swa_device_check(P.ctx) == 0
+
+
+@pytest.mark.parametrize("shape", [MIMO, TINY], ids=["mimo", "tiny"])
+def test_workspace_shared_with_decode_and_across_kernels(shape):
+    """One workspace, zeroed once, under tree attention on either kernel and
+    decode attention in turn: bits as with fresh ones."""
+    ps = 1 if shape is TINY else 64
+    P, S = _step(shape, ps, [2500, 333], _trees(20, [13, 7]))
+    d_seq, rows = S.d["seq"], S.d["rows"]
+    dplan = torch.zeros(api.swa_plan_bytes(P.ctx, 2, 1), dtype=torch.uint8, device="cuda")
+    api.swa_plan(P.ctx, P.rt, rows, None, d_seq, dplan, 1)
+    qs = [P.to_dev(S.queries(l)) for l in range(2)]
+    size = 0
+    for path in (-1, 0):
+        api.swa_set_attn_path(P.ctx, path)
+        size = max([size] + [S.workspace(l).numel() for l in range(2)]
+                   + [api.swa_attn_decode_ws_bytes(P.ctx, l, 2, S.max_seq) for l in range(2)])
+
+    def run(ws):
+        got = []
+        for path in (-1, 0, -1):
+            api.swa_set_attn_path(P.ctx, path)
+            for l in range(2):
+                out, dec = torch.empty_like(qs[l]), torch.empty_like(qs[l][:2])
+                S.run(l, qs[l], out, ws())
+                api.swa_attn_decode(P.ctx, l, P.rt, rows, d_seq, S.max_seq, dplan, qs[l][:2].contiguous(),
+                                    P.sinks_d[l], P.scale, dec, ws())
+                got += [out, dec]
+        return got
+
+    shared = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    want = run(lambda: torch.zeros(size, dtype=torch.uint8, device="cuda"))
+    for a, b in zip(run(lambda: shared), want):
+        assert torch.equal(a, b)
     assert api.swa_device_check(P.ctx) == 0
 
 
