@@ -43,9 +43,10 @@
 //     and i + 4 can read the same lanes).
 // E4M3 KV: K and V tiles arrive as bytes in a ring of their own; four more warps
 // turn them into f16 tiles (exact: E4M3 is a subset of f16) and each Q tile from
-// bf16 to f16 in place (with 16 warps the launch has 128 registers a thread, of
-// which the other roles give the softmax groups forty each: setmaxnreg); the products run on f16 operands, P is packed as f16,
-// the K scale joins the softmax scale and the V scale the output.
+// bf16 to f16 in place, the products run on f16 operands, P is packed as f16, the
+// K scale joins the softmax scale and the V scale the output.  (With 16 warps the
+// launch has 128 registers a thread; the other roles give the softmax groups 24
+// each, setmaxnreg.)
 // Key columns that some row may not read (window edge, non-ancestors) get -inf
 // scores from a 64-bit mask per row and 64-column chunk; chunks that no row of
 // a warp reads are skipped.
@@ -55,7 +56,6 @@
 #include <algorithm>
 
 #include <math.h>
-
 
 #include "spec_internal.h"
 #include "tc_ptx.cuh"
@@ -1098,13 +1098,25 @@ struct TreeWs {
 // [reserved][tickets] as in the other attention families, which this one leaves
 // untouched (so calls of either may share a workspace), then the descriptors and
 // partials.
-TreeWs tree_ws(const Ctx &c, int layer, int64_t nq, int max_new, int max_seq_len) {
+TreeWs tree_ws(const Ctx &c, int layer, int bs, int64_t nq, int max_new, int max_seq_len) {
   const LayerInfo &L = c.layers[layer];
   TreeWs w;
   const int G = c.cfg.num_q_heads / L.hkv, T = tile_nodes(c, layer, max_new);
   w.groups = std::max(1, (c.num_sms > 0 ? c.num_sms : 148) / L.hkv);
   w.rows = std::min(2 * T, max_new) * G;
-  w.whole = tree_max_keys(c, layer, max_new, max_seq_len) <= 512;
+  // Whole items or equal stretches of the keys?  Whole items save the batch scan,
+  // the partials and the merge; stretches keep every CTA busy.  Device time of
+  // plan and attention, 8 nodes, whole against stretches: 2 requests of 500 / 1000
+  // / 2000 / 4000 tokens 13.2 / 16.3 / 22.5 / 34.8 against 18.4 / 21.7 / 27.7 / 28.2
+  // us (MiMo full layer); 64 requests of up to 1000 / 2000 / 4000 / 8000 tokens 25.4
+  // / 43.8 / 75.5 / 129.5 against 39.6 / 54.9 / 77.5 / 120.0 us.  Where the items of
+  // a group come out uneven (40 requests on 19 groups: three for some, two for
+  // most) whole items lose from 2000 tokens on: 40.7 against 38.5 us (D = 64), 61.2
+  // against 54.3 us (E4M3).
+  const int64_t keys = tree_max_keys(c, layer, max_new, max_seq_len);
+  const int64_t items = (int64_t)bs * ((max_new + 2 * T - 1) / (2 * T));
+  const int64_t most = (items + w.groups - 1) / w.groups;
+  w.whole = keys <= 1024 || (keys <= 2048 && (most <= 1 || 4 * most * w.groups <= 5 * items));
   // whole 128-byte lines of four dims x 32 rows
   w.rows = (w.rows + 31) / 32 * 32;
   w.part_stride = (int64_t)w.rows * (c.cfg.head_dim + 2);
@@ -1154,14 +1166,15 @@ bool tc_tree_supported(const Ctx &c, int layer) {
           (c.cfg.kv_dtype == SWA_DTYPE_E4M3 && d == 128));
 }
 
-size_t tc_tree_ws_bytes(const Ctx &c, int layer, int64_t nq, int max_new, int max_seq_len) {
-  return (tree_ws(c, layer, nq, max_new, max_seq_len).total + 255) / 256 * 256;
+size_t tc_tree_ws_bytes(const Ctx &c, int layer, int bs, int64_t nq, int max_new,
+                        int max_seq_len) {
+  return (tree_ws(c, layer, bs, nq, max_new, max_seq_len).total + 255) / 256 * 256;
 }
 
 cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree, cudaStream_t s) {
   if (a.nq == 0) return cudaSuccess;
   const LayerInfo &L = c.layers[a.layer];
-  const TreeWs w = tree_ws(c, a.layer, a.nq, a.max_new, a.max_seq_len);
+  const TreeWs w = tree_ws(c, a.layer, a.bs, a.nq, a.max_new, a.max_seq_len);
   TreeParams P{};
   P.kind = L.kind;
   P.window = L.window;

@@ -777,7 +777,7 @@ size_t swa_attn_tree_ws_bytes(const swa_ctx *c, int32_t layer, int32_t bs, int64
   if (!c || layer < 0 || layer >= c->cfg.num_layers || bs < 0 || n_tokens < 0 || max_new < 1 ||
       max_new > SWA_TREE_MAX_NODES || max_seq_len < 1)
     return 0;
-  if (use_tree_tc(c, layer)) return swa::tc_tree_ws_bytes(*c, layer, n_tokens, max_new, max_seq_len);
+  if (use_tree_tc(c, layer)) return swa::tc_tree_ws_bytes(*c, layer, bs, n_tokens, max_new, max_seq_len);
   return swa::simt_tree_ws_bytes(*c, layer, n_tokens, max_new, max_seq_len);
 }
 

@@ -89,7 +89,8 @@ bool make_q_tile_map(CUtensorMap *m, const void *x, int64_t nq, int hq, int d, i
 
 // ---- attn_tree_tc.cu ------------------------------------------------------------
 bool tc_tree_supported(const Ctx &c, int layer);
-size_t tc_tree_ws_bytes(const Ctx &c, int layer, int64_t nq, int max_new, int max_seq_len);
+size_t tc_tree_ws_bytes(const Ctx &c, int layer, int bs, int64_t nq, int max_new,
+                        int max_seq_len);
 cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree, cudaStream_t s);
 
 // ---- qk_norm_rope.cu ----------------------------------------------------------

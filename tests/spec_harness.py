@@ -110,11 +110,18 @@ class TreeStep:
             mag.append(m)
         return np.array(at), np.concatenate(ref), np.concatenate(mag)
 
-    def check(self, layer, sinks=True, requests=None, what=""):
-        g, q = self.attend(layer, sinks)
+    def check(self, layer, sinks=True, requests=None, what="", bounds=(None, 8192)):
+        """Against the oracle, with each bound on the lengths (the caller's
+        max_seq_len; None: the longest sequence) - a large one makes the
+        tensor-core kernel split and merge the keys of short requests too."""
+        q = self.queries(layer)
         at, ref, mag = self.oracle(layer, q, sinks, requests)
-        assert_attention(g[at], ref, mag, self.P.dtype, f"{what} layer {layer}")
-        return g
+        exact = self.max_seq
+        for bound in bounds:
+            self.max_seq = bound or exact
+            g, _ = self.attend(layer, sinks)
+            assert_attention(g[at], ref, mag, self.P.dtype, f"{what} layer {layer} bound {bound}")
+        self.max_seq = exact
 
 
 def assert_attention(got, ref, mag, dtype, what=""):

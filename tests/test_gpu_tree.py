@@ -210,10 +210,12 @@ def test_wide_scores(shape, path):
     lens, _ = grow(P, [1, 2], [900, 420])
     S = TreeStep(P, [1, 2], lens, _trees(13, [14, 9]))
     for l in range(2):
-        g, q = S.attend(l)
-        at, ref, mag = S.oracle(l, q)
+        at, ref, mag = S.oracle(l, S.queries(l))
         tol = 2 * (2.0 ** -8 + 2.0 ** -6.5) * mag + 2.0 ** -8 * np.abs(ref) + 1e-6
-        assert np.isfinite(g).all() and (np.abs(g[at] - ref) <= tol).all(), f"layer {l}"
+        for bound in (S.max_seq, 8192):          # whole items; split and merged
+            S.max_seq = bound
+            g, _ = S.attend(l)
+            assert np.isfinite(g).all() and (np.abs(g[at] - ref) <= tol).all(), f"layer {l}"
     assert api.swa_device_check(P.ctx) == 0
 
 
@@ -223,10 +225,10 @@ def test_long_windows(shape):
     full layers, with a first column inside a page, and nodes on both sides of a
     chunk's border."""
     hkv = shape["layers"][1][2]
-    layers = [(OT.SLIDING, 1000, hkv), (OT.CHUNKED, 1500, hkv), (OT.SLIDING, 600, hkv)]
+    layers = [(OT.SLIDING, 2500, hkv), (OT.CHUNKED, 3000, hkv), (OT.SLIDING, 600, hkv)]
     rng = np.random.default_rng(18)
-    parents = [random_parents(rng, 14), list(range(-1, 14)), random_parents(rng, 5)]
-    P, S = _step(shape, 16, [4483, 1490, 20], parents, layers=layers)
+    parents = [random_parents(rng, 7), list(range(-1, 14)), random_parents(rng, 5)]
+    P, S = _step(shape, 16, [4483, 2990, 20], parents, layers=layers)
     for l in range(3):
         S.check(l, what="long window")
     assert api.swa_device_check(P.ctx) == 0
