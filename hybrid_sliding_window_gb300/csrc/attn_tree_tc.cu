@@ -651,36 +651,52 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       if (nd == 0 && !(wait_all(bar(B_PREADY), 0) && wait_all(bar(B_PREADY + 1), 0))) break;
       int ok = 1;
       if (elect_one()) {
+        // Ring slots (and phases) of the next K and V tile.
+        auto advance = [](int &slot, uint32_t &phase, int by) {
+          slot += by;
+          if (slot >= kStages) {
+            slot -= kStages;
+            phase ^= 1u;
+          }
+        };
+        int ks = base % kStages, vs = ks, kt = 0, vt = 0;   // slots; tiles of the segment
+        uint32_t kp = (base / kStages) & 1, vp = kp;
+        advance(vs, vp, min(2, 2 * n - 1));
         for (int u = -2; u < U; ++u) {       // u = -2, -1: S(0) and S(1) only
           const int g = u & 1;
+          const bool fresh = !shared || !g, last = !shared || g;   // first, last use of a tile
           if (u >= 0) {
-            const int r = base + seq_v(shared ? u >> 1 : u, n), s = r % kStages;
-            if (!(ok = mbar_wait(bar(B_FULL + s), (r / kStages) & 1, &s_abort))) break;
+            if (fresh && !(ok = mbar_wait_ready(bar(B_FULL + vs), vp, &s_abort))) break;
             if (!(ok = mbar_wait(bar(B_PREADY + g), ((g ? steps1 : steps0) + (u >> 1)) & 1, &s_abort)))
               break;
             tc_fence_after();
-            const uint64_t vd = dv + (uint64_t)(s * kTileBytes >> 4);
+            const uint64_t vd = dv + (uint64_t)(vs * kTileBytes >> 4);
 #pragma unroll
-            for (int ks = 0; ks < kKeys / 16; ++ks)
-              mma_ts(tmem + 256 + g * kD, tmem + g * 128 + ks * 8,
-                     vd + (uint64_t)(ks * 16 * 128 >> 4), kIdO, (u >= 2 || ks > 0) ? 1u : 0u);
-            if (!shared || g) tc_commit(bar(B_EMPTY + s));
+            for (int e = 0; e < kKeys / 16; ++e)
+              mma_ts(tmem + 256 + g * kD, tmem + g * 128 + e * 8,
+                     vd + (uint64_t)(e * 16 * 128 >> 4), kIdO, (u >= 2 || e > 0) ? 1u : 0u);
+            if (last) {
+              tc_commit(bar(B_EMPTY + vs));
+              advance(vs, vp, ++vt == n - 1 ? 1 : 2);
+            }
             if (u + 2 >= U) tc_commit(bar(B_ODONE + g));
             if (U == 1) tc_commit(bar(B_ODONE + 1));
           }
           if (u + 2 < U) {                   // S(u + 2), of the same group
-            const int r = base + seq_k(shared ? (u + 2) >> 1 : u + 2), s = r % kStages;
-            if (!(ok = mbar_wait(bar(B_FULL + s), (r / kStages) & 1, &s_abort))) break;
+            if (fresh && !(ok = mbar_wait_ready(bar(B_FULL + ks), kp, &s_abort))) break;
             tc_fence_after();
-            const uint64_t kd = dk + (uint64_t)(s * kTileBytes >> 4);
+            const uint64_t kd = dk + (uint64_t)(ks * kTileBytes >> 4);
             const uint64_t qd = dq + (uint64_t)((mode != kAlternate && g ? kTileBytes : 0) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks) {
-              const uint64_t off = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
-              mma_ss(tmem + g * 128, qd + off, kd + off, kIdS, ks > 0);
+            for (int e = 0; e < kD / 16; ++e) {
+              const uint64_t off = ((e >> 2) * kBlock + (e & 3) * 32) >> 4;
+              mma_ss(tmem + g * 128, qd + off, kd + off, kIdS, e > 0);
             }
             tc_commit(bar(B_SDONE + g));
-            if (!shared || g) tc_commit(bar(B_EMPTY + s));
+            if (last) {
+              tc_commit(bar(B_EMPTY + ks));
+              advance(ks, kp, kt++ == 0 ? 1 : 2);
+            }
             if (u + 3 == U) tc_commit(bar(B_QFREE));
           }
         }

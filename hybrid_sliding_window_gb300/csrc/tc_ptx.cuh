@@ -56,6 +56,18 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   *abort_flag = 1;
   return false;
 }
+// The same for a phase that has mostly completed already: one plain test first.
+__device__ __forceinline__ bool mbar_wait_ready(uint32_t bar, uint32_t parity,
+                                                volatile int *abort_flag) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done || mbar_wait(bar, parity, abort_flag);
+}
 // Bounded wait used only after an abort, for work that completes on its own
 // (issued TMA loads, committed tensor-core products): it ignores the flag.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
