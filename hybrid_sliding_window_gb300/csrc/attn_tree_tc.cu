@@ -454,14 +454,17 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
 
     auto bcast = [&](int x, int l) { return __shfl_sync(0xffffffffu, x, l); };
     if (P.whole) {
-      // The head's line of blocks, every request's the same number of them (some
-      // empty), so nothing is summed up; this CTA's stretch of it, 32 at a time.
+      // The head's blocks, every request's the same number of them (some empty),
+      // so nothing is summed up: neighbours to a CTA where a request has one, in
+      // turn where it may have more (a large tree among small ones is spread).
+      // This CTA's, 32 at a time.
       const unsigned per = P.blocks, total = P.bs * per, share = (total + P.groups - 1) / P.groups;
-      const unsigned w0 = group_id * share, w1 = min(total, w0 + share);
-      for (unsigned x0 = w0; ok && x0 < w1; x0 += 32) {
-        const unsigned x = x0 + lane;
+      const unsigned step = per == 1 ? 1 : P.groups, x_lo = per == 1 ? group_id * share : group_id;
+      const unsigned x_hi = per == 1 ? min(total, x_lo + share) : total;
+      for (unsigned x0 = x_lo; ok && x0 < x_hi; x0 += 32 * step) {
+        const unsigned x = x0 + lane * step;
         const int b = per == 1 ? x : x / per, blk = x - b * per;
-        const Request r = request(P, x < w1 ? b : P.bs);
+        const Request r = request(P, x < x_hi ? b : P.bs);
         Piece mp{b, blk * 2 * T, min(2 * T, r.n - blk * 2 * T), r.q0 + blk * 2 * T, r.col0, r.prefix};
         const int tiles = mp.n_tok > 0 ? block_tiles(P, r, blk) : 0;
         unsigned hit = __ballot_sync(0xffffffffu, mp.n_tok > 0);

@@ -651,7 +651,10 @@ swa_status swa_tree_plan(swa_ctx *ctx, int32_t bs, const int32_t *parents,
  * swa_tree_plan, `plan` (SWA-pool layers) from swa_plan with the same
  * prefix_lens, seq = prefix + nodes and the same max_new; max_seq_len bounds
  * seq.  q, out: [n_tokens][Hq][D], f32 for an F32 pool, bf16 otherwise; q, out,
- * tree, plan and ws are 16-byte aligned.  Rows of entries that belong to no request are left as they are.
+ * tree, plan and ws are 16-byte aligned.  The tcgen05 kernel serves bf16 pools
+ * with head_dim 64 or 128 and E4M3 pools with head_dim 128 on pages of 16 to 64;
+ * other configurations run the generic kernel, which takes at most 65535
+ * entries.  Both give the same bits from run to run.  Rows of entries that belong to no request are left as they are.
  * `ws` as for swa_attn_decode (zero before its first use, reusable, also by
  * swa_attn_decode; calls that may overlap on the GPU need their own). */
 size_t swa_attn_tree_ws_bytes(const swa_ctx *ctx, int32_t layer, int32_t bs,
@@ -683,7 +686,8 @@ swa_status swa_attn_tree(swa_ctx *ctx, int32_t layer, int32_t bs,
  * rot_dim 0 rotates nothing (positions, cos_sin unused); otherwise it is a
  * multiple of 16 up to D.  positions may be swa_tree_plan's.  A position
  * outside the table sets SWA_DEVERR_RANGE and leaves the token's outputs and
- * slots as they were; a slot outside the pool sets it and is not written. */
+ * slots as they were; a slot outside the pool sets it and is not written.  Of
+ * two tokens with one slot either may stay, as in swa_store_kv. */
 swa_status swa_qk_norm_rope_store(swa_ctx *ctx, int32_t layer, const void *q,
                                   int64_t q_stride, const void *k,
                                   int64_t k_stride, const void *v,
@@ -725,12 +729,12 @@ swa_status swa_copy_kv(swa_ctx *ctx, const int64_t *src, const int64_t *dst,
 
 /* Which kernel family the last attention call on ctx launched
  * (0 = generic CUDA-core kernel, 1 = tensor-core decode fed by cp.async,
- * 2 = tcgen05 extend), for tests and profiling. */
+ * 2 = tcgen05 extend, 3 = tcgen05 tree attention), for tests and profiling. */
 int32_t swa_last_attn_path(const swa_ctx *ctx);
 /* Restricts the kernel family attention calls on ctx may take: -1 = best
- * available (default: cp.async tensor-core decode, tcgen05 extend), 0 =
- * generic CUDA-core kernel only, 1 = cp.async tensor-core decode and no
- * tcgen05 extend.  Any other value is SWA_ERR_INVALID.  For tests and
+ * available (default: cp.async tensor-core decode, tcgen05 extend and tree
+ * attention), 0 = generic CUDA-core kernel only, 1 = cp.async tensor-core
+ * decode and no tcgen05 kernel.  Any other value is SWA_ERR_INVALID.  For tests and
  * profiling. */
 swa_status swa_set_attn_path(swa_ctx *ctx, int32_t path);
 
