@@ -1036,7 +1036,7 @@ def spec_alloc_rate(st):
 # from an ncu capture and stored under profiles/, is reported only while
 # these files are unchanged since the capture.
 DECODE_SOURCES = ("attn_decode_mma.cu", "split_merge.cuh", "kv_codec.cuh", "swa_internal.h")
-EXTEND_SOURCES = ("attn_extend_tc.cu", "swa_internal.h")
+EXTEND_SOURCES = ("attn_extend_tc.cu", "tc_ptx.cuh", "swa_internal.h")
 
 
 def kernel_hash(files):
