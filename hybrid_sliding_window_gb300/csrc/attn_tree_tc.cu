@@ -1,6 +1,6 @@
 // Draft-tree attention on the 5th-generation tensor cores (tcgen05 + TMEM + TMA):
-// bf16 KV with D = 64 or 128, or E4M3 KV with D = 128; any GQA group, page size
-// 16..64.
+// bf16 KV with D = 64 or 128, or E4M3 KV with D = 128; any GQA group and page
+// size.
 //
 // Method: node i of a request reads the cached columns of its window and its
 // ancestors' columns behind the prefix (include/swa.h, swa_attn_tree).  With T
@@ -32,6 +32,9 @@
 //     which the products use them.  (One warp for both: a TMA box costs its
 //     issuing thread 75 to 100 cycles, sixteen of them per tile pair on pages
 //     of 16 rows, which was the pace of such layers.)
+//     Pages that are no TMA box (fewer than 16 rows, more than 64, no power of
+//     two) are gathered instead: the same two warps look up a row per key and copy
+//     it with 16-byte cp.async into the same layout, 64 copies a lane and tile.
 //   * warp 10 loads each segment's Q tiles once the previous segment's last
 //     QK^T has read them;
 //   * warp 8 issues S = Q K^T and O += P V with P in TMEM over S;
@@ -92,6 +95,7 @@ struct TreeGeo {
 struct TreeParams {
   int kind, window, hkv, G, T, ps, ps_shift;   // T: nodes of a Q tile
   int64_t page_stride, pool_rows;
+  KvAddr addr;               // gathered pages: where rows live
   const int32_t *rt;
   int64_t rt_stride;
   const int64_t *req_idx, *pre, *qo_indptr;
@@ -241,7 +245,7 @@ __device__ __forceinline__ int tile_off(int r, int c) {
   return (c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-template <int kD, bool kF8>
+template <int kD, bool kF8, bool kGather>
 __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     k_tree_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
               const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TreeParams P) {
@@ -301,11 +305,11 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     mbar_init(bar(B_EPI), 2 * kTileRows);
     mbar_init(bar(B_DRAIN), 1);
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(B_FULL + i), kF8 ? kConvThreads : 1);
+      mbar_init(bar(B_FULL + i), kF8 ? kConvThreads : kGather ? 32 : 1);
       mbar_init(bar(B_EMPTY + i), 1);
     }
     for (int i = 0; i < Gm::kRawStages; ++i) {
-      mbar_init(bar(B_RAWFULL + i), 1);
+      mbar_init(bar(B_RAWFULL + i), kGather ? 32 : 1);
       mbar_init(bar(B_RAWEMPTY + i), kConvThreads / 32);
     }
     mbar_init(bar(B_QCONV), kConvThreads);
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
   // Warp-collective: the K tiles (warp 9) or the V tiles (warp 11) of a segment
   // whose first tile has position `base` in the ring of the loads.
   const bool full_layer = P.kind == SWA_LAYER_FULL;
-  const int ppt = kKeys >> P.ps_shift;       // pages per key tile
+  const int ppt = kGather ? 1 : kKeys >> P.ps_shift;   // pages per key tile
   auto stream = [&](const Segment &sg, int base) {
     const bool pair = sg.mode == kPair;
     // Page records and rows of piece w: 32 page slots at a time, lane i slot i.
@@ -416,6 +420,76 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     return true;
   };
 
+  // The same by 16-byte copies of every key's row.
+  auto gather = [&](const Segment &sg, int base) {
+    constexpr int kChunks = (kF8 ? kD : 2 * kD) / 16;      // of a head's row
+    const bool pair = sg.mode == kPair, is_v = warp == 11;
+    const int n = ring_tiles(sg.mode, sg.n_tiles);
+    // Rows of the ring's tile x: lane i those of columns i, 32 + i, ...  Columns
+    // behind the last one read it again (finite values, zero weight).
+    auto slots_of = [&](int x, int64_t (&slot)[4]) {
+      const Piece pc = pair && (x & 1) ? sg.piece[1] : sg.piece[0];
+      const int hi = pc.prefix + pc.n0 + pc.n_tok - 1;
+      const int first = max(pc.prefix - P.lookback, 0) / P.ps;   // the plan's first page
+      const int32_t *rt_row = full_layer ? P.rt + P.req_idx[pc.b] * P.rt_stride : nullptr;
+      const int4 h = full_layer ? make_int4(0, 0, 0, 0)
+                                : *reinterpret_cast<const int4 *>(P.plan.hdr + pc.b * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = min(pc.col0 + (pair ? x >> 1 : x) * kKeys + 32 * i + lane, hi);
+        if (full_layer) {
+          slot[i] = rt_row[col];
+        } else {
+          const int pg = col / P.ps, k = pg - first;
+          const bool in = k >= 0 && k < P.plan.max_pages && k < h.w && col >= h.x && h.z == first;
+          const int32_t page = in ? P.plan.pages[(int64_t)pc.b * P.plan.max_pages + k] : -1;
+          if (page == 0) set_error(P.err, SWA_DEVERR_WINDOW_EVICTED);
+          slot[i] = page < 0 ? -1 : (int64_t)page * P.ps + (col - pg * P.ps);
+        }
+      }
+    };
+    const char *pool = (is_v ? P.addr.v : P.addr.k) + kvh * (kChunks * 16);
+    int64_t next[4];
+    slots_of(0, next);
+    for (int t = 0; t < n; ++t) {
+      int64_t from[4];                       // byte offsets of this lane's rows
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int64_t slot = next[i];
+        if (slot < 0 || slot >= P.pool_rows) {
+          set_error(P.err, SWA_DEVERR_RANGE);
+          slot = 0;
+        }
+        from[i] = kv_row(P.addr, slot) * P.addr.row_bytes;
+      }
+      __syncwarp();
+      if (t + 1 < n) slots_of(t + 1, next);  // in flight while this tile is copied
+      const int pos = base + (is_v ? seq_v(t, n) : seq_k(t)), s = pos % kLoads, f = pos / kLoads;
+      if (f >= 1 && !wait_all(bar(bLoadEmpty + s), (f - 1) & 1)) return false;
+      const uint32_t dst = sb + kOffLoad + s * kLoadBytes;
+      const int c = lane % kChunks;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll 4
+        for (int q = 0; q < kChunks; ++q) {
+          const int e = q * (32 / kChunks) + lane / kChunks;   // row of the 32
+          const char *src = pool + __shfl_sync(0xffffffffu, from[i], e) + c * 16;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(
+                           dst + tile_off(32 * i + e, c)),
+                       "l"(src)
+                       : "memory");
+        }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(
+                       bar(bLoadFull + s))
+                   : "memory");
+    }
+    return true;
+  };
+  auto load_tiles = [&](const Segment &sg, int base) {
+    if constexpr (kGather) return gather(sg, base);
+    else return stream(sg, base);
+  };
+
   if (warp >= 8) {
   // E4M3 KV: 512 threads x 128 registers = 256 x 152 (softmax) + 256 x 104; whole
   // warpgroups on each side.
@@ -447,7 +521,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       sg.part = part;
       sg.piece[0] = p0;
       sg.piece[1] = p1;
-      const bool good = publish(sg) && stream(sg, base);
+      const bool good = publish(sg) && load_tiles(sg, base);
       base += 2 * ring_tiles(mode, n);
       return good;
     };
@@ -561,7 +635,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       const Segment sg = s_seg[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_IEMPTY + slot));
-      if (sg.mode < 0 || !(warp == 10 ? load_q(sg, nd) : stream(sg, base))) break;
+      if (sg.mode < 0 || !(warp == 10 ? load_q(sg, nd) : load_tiles(sg, base))) break;
       base += 2 * ring_tiles(sg.mode, sg.n_tiles);
     }
   } else if (warp >= 12) {
@@ -670,6 +744,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
           const bool fresh = !shared || !g, last = !shared || g;   // first, last use of a tile
           if (u >= 0) {
             if (fresh && !(ok = mbar_wait_ready(bar(B_FULL + vs), vp, &s_abort))) break;
+            if (kGather && !kF8) fence_async_smem();   // copied through the generic proxy
             if (!(ok = mbar_wait(bar(B_PREADY + g), ((g ? steps1 : steps0) + (u >> 1)) & 1, &s_abort)))
               break;
             tc_fence_after();
@@ -687,6 +762,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
           }
           if (u + 2 < U) {                   // S(u + 2), of the same group
             if (fresh && !(ok = mbar_wait_ready(bar(B_FULL + ks), kp, &s_abort))) break;
+            if (kGather && !kF8) fence_async_smem();
             tc_fence_after();
             const uint64_t kd = dk + (uint64_t)(ks * kTileBytes >> 4);
             const uint64_t qd = dq + (uint64_t)((mode != kAlternate && g ? kTileBytes : 0) >> 4);
@@ -1028,6 +1104,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       }
     }
   }
+  if (kGather) asm volatile("cp.async.wait_all;\n" ::: "memory");
   // Every role has left its loop: s_abort is final.
   __syncthreads();
   if (s_abort) {
@@ -1146,7 +1223,7 @@ TreeWs tree_ws(const Ctx &c, int layer, int bs, int64_t nq, int max_new, int max
   return w;
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool G>
 cudaError_t launch_tree(const LayerInfo &L, const CUtensorMap &tmq, const TreeParams &P, int rows,
                         int device, cudaStream_t s) {
   using Gm = TreeGeo<D, F8>;
@@ -1154,7 +1231,7 @@ cudaError_t launch_tree(const LayerInfo &L, const CUtensorMap &tmq, const TreePa
   static_assert(B_COUNT == 40 && Gm::kOffCtl + sizeof(Control) <= 227 * 1024,
                 "shared memory of a CTA");
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(k_tree_tc<D, F8>, smem, device, done);
+  cudaError_t e = allow_smem(k_tree_tc<D, F8, G>, smem, device, done);
   if (e != cudaSuccess) return e;
   const int ctas = P.groups * P.hkv;
   cudaLaunchAttribute attr;
@@ -1167,7 +1244,7 @@ cudaError_t launch_tree(const LayerInfo &L, const CUtensorMap &tmq, const TreePa
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k_tree_tc<D, F8>, L.tmk, L.tmv, tmq, P);
+  e = cudaLaunchKernelEx(&cfg, k_tree_tc<D, F8, G>, L.tmk, L.tmv, tmq, P);
   if (e != cudaSuccess || P.whole) return e;
   cfg.gridDim = dim3((rows + kMergeRows - 1) / kMergeRows, ctas);
   cfg.blockDim = dim3(kMergeThreads);
@@ -1177,10 +1254,15 @@ cudaError_t launch_tree(const LayerInfo &L, const CUtensorMap &tmq, const TreePa
 
 }  // namespace
 
+// Pages that are TMA boxes of the layer's tensor maps.
+static bool boxed_pages(const Ctx &c, int layer) {
+  return c.layers[layer].tma && c.cfg.page_size <= 64;
+}
+
 bool tc_tree_supported(const Ctx &c, int layer) {
-  const LayerInfo &L = c.layers[layer];
+  const KvAddr &a = c.layers[layer].addr;
   const int d = c.cfg.head_dim;
-  return L.tma && c.cfg.page_size <= 64 &&
+  return ((reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 15) == 0 &&
          ((c.cfg.kv_dtype == SWA_DTYPE_BF16 && (d == 64 || d == 128)) ||
           (c.cfg.kv_dtype == SWA_DTYPE_E4M3 && d == 128));
 }
@@ -1201,7 +1283,9 @@ cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree,
   P.G = c.cfg.num_q_heads / L.hkv;
   P.T = tile_nodes(c, a.layer, a.max_new);
   P.ps = c.cfg.page_size;
-  P.ps_shift = __builtin_ctz((unsigned)P.ps);
+  const bool boxed = boxed_pages(c, a.layer);
+  P.ps_shift = boxed ? __builtin_ctz((unsigned)P.ps) : 0;
+  P.addr = L.addr;
   P.page_stride = (int64_t)P.ps * (L.addr.blocks ? L.addr.blocks : 1);
   P.pool_rows = (L.in_full ? c.cfg.size_full : c.cfg.size_swa) + c.cfg.page_size;
   P.rt = a.rt;
@@ -1233,9 +1317,13 @@ cudaError_t launch_attn_tree_tc(Ctx &c, const AttnArgs &a, const TreeView &tree,
   CUtensorMap tmq;
   if (!make_q_tile_map(&tmq, a.q, a.nq, c.cfg.num_q_heads, c.cfg.head_dim, P.G, P.T))
     return cudaErrorInvalidValue;
-  if (f8) return launch_tree<128, true>(L, tmq, P, w.rows, c.device, s);
-  return c.cfg.head_dim == 64 ? launch_tree<64, false>(L, tmq, P, w.rows, c.device, s)
-                              : launch_tree<128, false>(L, tmq, P, w.rows, c.device, s);
+  auto go = [&](auto gather) {
+    constexpr bool g = decltype(gather)::value;
+    if (f8) return launch_tree<128, true, g>(L, tmq, P, w.rows, c.device, s);
+    return c.cfg.head_dim == 64 ? launch_tree<64, false, g>(L, tmq, P, w.rows, c.device, s)
+                                : launch_tree<128, false, g>(L, tmq, P, w.rows, c.device, s);
+  };
+  return boxed ? go(std::false_type{}) : go(std::true_type{});
 }
 
 }  // namespace swa

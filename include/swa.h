@@ -652,9 +652,9 @@ swa_status swa_tree_plan(swa_ctx *ctx, int32_t bs, const int32_t *parents,
  * prefix_lens, seq = prefix + nodes and the same max_new; max_seq_len bounds
  * seq.  q, out: [n_tokens][Hq][D], f32 for an F32 pool, bf16 otherwise; q, out,
  * tree, plan and ws are 16-byte aligned.  The tcgen05 kernel serves bf16 pools
- * with head_dim 64 or 128 and E4M3 pools with head_dim 128 on pages of 16 to 64;
- * other configurations run the generic kernel, which takes at most 65535
- * entries.  Both give the same bits from run to run.  Rows of entries that belong to no request are left as they are.
+ * with head_dim 64 or 128 and E4M3 pools with head_dim 128, at any page size
+ * (16, 32 and 64 fastest); other configurations run the generic kernel, which
+ * takes at most 65535 entries.  Both give the same bits from run to run.  Rows of entries that belong to no request are left as they are.
  * `ws` as for swa_attn_decode (zero before its first use, reusable, also by
  * swa_attn_decode; calls that may overlap on the GPU need their own). */
 size_t swa_attn_tree_ws_bytes(const swa_ctx *ctx, int32_t layer, int32_t bs,

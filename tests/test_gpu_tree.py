@@ -109,6 +109,11 @@ CASES = [
     pytest.param(MIMO, 64, "per_layer", id="mimo-ps64"),
     pytest.param(MIMO, 16, "per_layer", id="mimo-ps16"),
     pytest.param(MIMO, 1, "per_layer", id="mimo-ps1"),
+    pytest.param(MIMO, 48, "per_layer", id="mimo-ps48"),
+    pytest.param(MIMO, 128, "per_layer", id="mimo-ps128"),
+    pytest.param(GPTOSS, 8, "envelope", id="gptoss-envelope-ps8"),
+    pytest.param(LLAMA4, 4, "envelope", id="llama4-envelope-ps4"),
+    pytest.param(LLAMA4, 1, "per_layer", id="llama4-ps1"),
     pytest.param(GPTOSS, 16, "per_layer", id="gptoss-ps16"),
     pytest.param(GPTOSS, 32, "envelope", id="gptoss-envelope-ps32"),
     pytest.param(LLAMA4, 64, "envelope", id="llama4-envelope-ps64"),
@@ -184,6 +189,25 @@ def test_one_long_request(shape, nodes):
             mag.append(OT.attend_heads(q[i], K, np.abs(V), P.sinks[l], P.scale))
         assert_attention(g[some], np.stack(ref), np.stack(mag), P.dtype, f"{nodes} nodes layer {l}")
     assert api.swa_device_check(P.ctx) == 0
+
+
+@pytest.mark.parametrize("shape", [MIMO, LLAMA4], ids=["mimo", "llama4"])
+@pytest.mark.parametrize("ps", [1, 20])
+def test_gathered_pages(shape, ps):
+    """Pages that are gathered key by key: many tiles, items in pairs, blocks of
+    several Q tiles, rows of nobody and an evicted page."""
+    P, S = _step(shape, ps, [1500, 130, 40, 1], _trees(21, [40, 5, 21, 1]))
+    for l in range(2):
+        S.check(l, what=f"ps {ps}")
+    assert api.swa_last_attn_path(P.ctx) == 3
+    assert api.swa_device_check(P.ctx) == 0
+    page = int(P.ort[1, 1495]) // ps * ps
+    keep = P.ctx.mapping()[page:page + ps].clone()
+    P.ctx.mapping()[page:page + ps] = 0
+    S.make_plans()
+    S.attend(0)
+    assert api.swa_device_check(P.ctx) & api.SWA_DEVERR_WINDOW_EVICTED
+    P.ctx.mapping()[page:page + ps] = keep
 
 
 @pytest.mark.parametrize("path", [-1, 0])
@@ -453,11 +477,11 @@ def test_device_checks():
     assert api.swa_device_check(P.ctx) == 0
 
 
-@pytest.mark.parametrize("shape,ps,kernel", [(MIMO, 64, 3), (MIMO, 16, 3), (MIMO, 1, 0), (GPTOSS, 32, 3),
+@pytest.mark.parametrize("shape,ps,kernel", [(MIMO, 64, 3), (MIMO, 16, 3), (MIMO, 1, 3), (GPTOSS, 32, 3),
                                              (LLAMA4, 64, 3), (TINY, 1, 0)],
                          ids=["mimo-ps64", "mimo-ps16", "mimo-ps1", "gptoss", "llama4", "tiny"])
 def test_kernel_taken(shape, ps, kernel):
-    """The tensor-core kernel serves bf16 and E4M3 pages of 16 to 64; -1 and 0 select."""
+    """The tensor-core kernel serves bf16 and E4M3 pools; -1 and 0 select."""
     P, S = _step(shape, ps, [40], [[-1, 0, 0]])
     S.attend(1)
     assert api.swa_last_attn_path(P.ctx) == kernel
