@@ -34,7 +34,9 @@
 //     of 16 rows, which was the pace of such layers.)
 //     Pages that are no TMA box (fewer than 16 rows, more than 64, no power of
 //     two) are gathered instead: the same two warps look up a row per key and copy
-//     it with 16-byte cp.async into the same layout, 64 copies a lane and tile.
+//     it with 16-byte cp.async into the same layout, 64 copies a lane and tile
+//     (16 requests of 4K to 32K tokens, full layer: 172 us on pages of 1 or 8, 114
+//     on pages of 16 or 64, 24.7 ms on the generic kernel).
 //   * warp 10 loads each segment's Q tiles once the previous segment's last
 //     QK^T has read them;
 //   * warp 8 issues S = Q K^T and O += P V with P in TMEM over S;
@@ -56,6 +58,18 @@
 // Every mbarrier wait has a poll limit; on expiry the kernel sets
 // SWA_DEVERR_TIMEOUT, every role leaves its loop, loads and products in flight
 // are waited for, and the TMEM is released.
+//
+// Measured (device time with the plan; floors at 6788 GB/s and 1946 TFLOP/s):
+// MiMo full layer, 64 requests of 4K to 32K tokens, 8 nodes: 408 us (6.77 TB/s,
+// floor 407); D = 64, 128 ragged trees of up to 13 nodes: 266 us (5.9 TB/s, floor
+// 231); one request of 131072 tokens, 64 nodes: 202 us (1360 TFLOP/s, floor 141);
+// E4M3, 4 x 131072 tokens, 16 nodes: 242 us (4.4 TB/s, floor 158); sliding layer,
+// 64 requests, 8 nodes: 22 us (floor 7.7).  Past the cache's bytes the bound is a
+// softmax group's loop - softmax of a tile (about 1600 cycles), its PV and its
+// next S, which overwrites P - of which two run in turn; TMEM holds no third.
+// E4M3 tiles also pass shared memory twice (conversions left out: 210 us).
+// Sliding layers are latency: 8 us for one request, 7.4 us for each further pair
+// of items of a CTA.
 #include <algorithm>
 
 #include <math.h>

@@ -8,7 +8,8 @@
 // HBM: bytes read + bytes written.  A warp moves 512 bytes at a time (32 lanes x
 // 16 bytes, coalesced both ways), looks the slots of up to 32 moves up with its
 // lanes in one go, and keeps kAhead loads in flight before it stores any.  A copy
-// of many rows gives a warp one 512-byte column of one layer's K or V rows; a
+// of many rows gives a warp one 512-byte column of one layer's K or V rows (1504
+// rows of 48 layers, 536 MB: 82.6 us, 6.5 TB/s, 96 % of the copy peak); a
 // commit has few rows per request, so there a warp takes whole K and V rows of a
 // layer and the chain of lookups (length, row, two slots, two mappings) is paid
 // once for all of them (64 requests, 48 layers, 65 MB: 15.1 -> 10.6 us).

@@ -23,6 +23,10 @@
 // whose bracketed factors a lane computes once per token (its dims are the same
 // in every row), so an element costs a product, a fused product-sum and the
 // product with rs, two elements at a time (f32x2).
+// Measured: 32768 tokens of 64 + 8 + 8 heads, bf16 D = 128 (1.36 GB): 239 us, 5.7
+// TB/s (84 % of the copy peak; issue slots 65 % busy); 512 tokens of 64 + 4 + 4:
+// 6.4 us; 4099 tokens of 40 + 8 + 8, E4M3 pool: 26.4 us (the divisions by the
+// scale, and 6.7 tokens per CTA).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
