@@ -6,13 +6,15 @@
 // full_to_swa[slot] on the others ("SWA in SGLang" design note, "two pools and
 // the mapping"), K and V of every layer.  The moves are pure copies, bound by
 // HBM: bytes read + bytes written.  A warp moves 512 bytes at a time (32 lanes x
-// 16 bytes, coalesced both ways), looks the slots of up to 32 moves up with its
-// lanes in one go, and keeps kAhead loads in flight before it stores any.  A copy
-// of many rows gives a warp one 512-byte column of one layer's K or V rows (1504
-// rows of 48 layers, 536 MB: 82.6 us, 6.5 TB/s, 96 % of the copy peak); a
-// commit has few rows per request, so there a warp takes whole K and V rows of a
-// layer and the chain of lookups (length, row, two slots, two mappings) is paid
-// once for all of them (64 requests, 48 layers, 65 MB: 15.1 -> 10.6 us).
+// 16 bytes, coalesced both ways), looks the slots of its moves up with its lanes
+// in one go, and keeps kAhead loads in flight before it stores any.  A copy gives
+// a warp one 512-byte column of one layer's K or V rows for kAhead moves (48
+// layers: 100 rows 5.8 us, 1504 rows, 536 MB, 80.8 us, 6.6 TB/s; with 32 moves a
+// warp 7.4 and 82.6 us).  A commit has few rows per request, so there a warp takes
+// whole rows of one layer's K or V, and the chain of lookups (length, row, two
+// slots, two mappings) is paid once for all their columns (48 layers: 64 requests,
+// 65 MB, 10.0 us, with a warp per column 15.1 us; 16 requests of 12 nodes, 7.4 us,
+// with K and V both on one warp 11.6 us).
 #include <cuda_runtime.h>
 
 #include "spec_internal.h"
@@ -22,7 +24,7 @@ namespace {
 
 constexpr int kMoveLayers = 64;    // layers per launch (the table is a kernel parameter)
 constexpr int kMoveWarps = 4;
-constexpr int kAhead = 8;          // rows in flight per warp
+constexpr int kAhead = 8;          // loads in flight per warp; moves of a copying warp
 
 struct MoveLayer {
   char *k, *v;
@@ -103,31 +105,31 @@ __device__ __forceinline__ void run_moves(char *base, int64_t col, bool in_row, 
   }
 }
 
-// grid: x = 32-move batches x 512-byte columns, y = 2 x layer + (K or V)
+// grid: x = batches of kAhead moves x 512-byte columns, y = 2 x layer + (K or V)
 __global__ void __launch_bounds__(kMoveWarps * 32)
     k_copy_kv(const __grid_constant__ MoveParams P, int cols) {
   const int lane = threadIdx.x & 31;
   const int64_t w = blockIdx.x * (int64_t)kMoveWarps + (threadIdx.x >> 5);
   const MoveLayer &L = P.layer[blockIdx.y >> 1];
-  const int64_t i = (w / cols) * 32 + lane;
+  const int64_t i = (w / cols) * kAhead + lane;
   const int64_t col = (w % cols) * 512 + lane * 16;
-  if ((w / cols) * 32 >= P.n || (w % cols) * 512 >= L.row_bytes) return;
+  if ((w / cols) * kAhead >= P.n || (w % cols) * 512 >= L.row_bytes) return;
   int64_t ra = 0, rb = 0;
   bool live = false;
-  if (i < P.n) {
+  if (lane < kAhead && i < P.n) {
     const int64_t a = P.src[i], b = P.dst[i];
     live = a != -1 && b != -1 && move_rows(P, L, a, b, ra, rb);
   }
   run_moves((blockIdx.y & 1) ? L.v : L.k, col, col < L.row_bytes, live, ra, rb);
 }
 
-// The same for whole K and V rows: 2 x cols columns per move, in move order, so
-// that every column sees its moves in lane order.
-__device__ __forceinline__ void run_row_moves(char *k, char *v, int row_bytes, int lane, bool live,
+// The same for whole rows: their columns, in move order, so that every column
+// sees its moves in lane order.
+__device__ __forceinline__ void run_row_moves(char *rows, int row_bytes, int lane, bool live,
                                               int64_t ra, int64_t rb) {
-  const int cols = (row_bytes + 511) / 512;
+  const int end = (row_bytes + 511) / 512 * 512;
   unsigned todo = __ballot_sync(0xffffffffu, live);
-  int l = todo ? __ffs(todo) - 1 : 0, seg = 0;   // move, column of it (K's, then V's)
+  int l = todo ? __ffs(todo) - 1 : 0, col = 0;   // move, column of it
   while (todo) {
     uint4 x[kAhead];
     char *to[kAhead];
@@ -135,15 +137,14 @@ __device__ __forceinline__ void run_row_moves(char *k, char *v, int row_bytes, i
     for (int u = 0; u < kAhead; ++u) {
       to[u] = nullptr;
       if (todo) {
-        const int c = seg < cols ? seg : seg - cols;
-        char *base = (seg < cols ? k : v) + c * 512 + lane * 16;
+        char *base = rows + col + lane * 16;
         const int64_t from = __shfl_sync(0xffffffffu, ra, l), dst = __shfl_sync(0xffffffffu, rb, l);
-        if (c * 512 + lane * 16 < row_bytes) {
+        if (col + lane * 16 < row_bytes) {
           x[u] = *reinterpret_cast<const uint4 *>(base + from);
           to[u] = base + dst;
         }
-        if (++seg == 2 * cols) {
-          seg = 0;
+        if ((col += 512) == end) {
+          col = 0;
           todo &= todo - 1;
           l = todo ? __ffs(todo) - 1 : 0;
         }
@@ -155,17 +156,17 @@ __device__ __forceinline__ void run_row_moves(char *k, char *v, int row_bytes, i
   }
 }
 
-// grid: x = requests, y = layer.  Node accepted[j] >= j moves to column prefix +
-// j.  Ascending order makes the moves safe in place: a move writes a column
-// below every later source, and its own source is only overwritten by a later
-// move - whose stores follow this warp's loads of the earlier moves (batches go
-// in order; within a batch loads precede stores), and no other warp touches
+// grid: x = requests, y = 2 x layer + (K or V).  Node accepted[j] >= j moves to
+// column prefix + j.  Ascending order makes the moves safe in place: a move writes
+// a column below every later source, and its own source is only overwritten by a
+// later move - whose stores follow this warp's loads of the earlier moves (batches
+// go in order; within a batch loads precede stores), and no other warp touches
 // these bytes.
 __global__ void __launch_bounds__(kMoveWarps * 32)
     k_commit_tree(const __grid_constant__ MoveParams P, int bs) {
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
-  const MoveLayer &L = P.layer[blockIdx.y];
+  const MoveLayer &L = P.layer[blockIdx.y >> 1];
   if (b >= bs) return;
   const int64_t pre = P.prefix[b];
   const int32_t *row = P.rt + P.req_idx[b] * P.rt_stride;
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
     int64_t ra = 0, rb = 0;
     bool live = j < n && (!wrong || lane < __ffs(wrong) - 1) && a != j;
     if (live) live = move_rows(P, L, row[pre + a], row[pre + j], ra, rb);
-    run_row_moves(L.k, L.v, L.row_bytes, lane, live, ra, rb);
+    run_row_moves((blockIdx.y & 1) ? L.v : L.k, L.row_bytes, lane, live, ra, rb);
     if (wrong) {
       set_error(P.err, SWA_DEVERR_RANGE);
       return;
@@ -234,7 +235,7 @@ cudaError_t launch_copy_kv(Ctx &c, const int64_t *src, const int64_t *dst, int64
   P.dst = dst;
   P.n = n;
   return for_layers(c, P, [&](const MoveParams &p, int nl, int cols) {
-    const int64_t warps = (n + 31) / 32 * cols;
+    const int64_t warps = (n + kAhead - 1) / kAhead * cols;
     dim3 grid((unsigned)((warps + kMoveWarps - 1) / kMoveWarps), 2 * nl);
     k_copy_kv<<<grid, kMoveWarps * 32, 0, s>>>(p, cols);
   });
@@ -254,7 +255,7 @@ cudaError_t launch_commit_tree(Ctx &c, int bs, const int32_t *rt, int64_t rt_str
   P.n_accepted = n_accepted;
   P.max_accept = max_accept;
   return for_layers(c, P, [&](const MoveParams &p, int nl, int) {
-    dim3 grid((bs + kMoveWarps - 1) / kMoveWarps, nl);
+    dim3 grid((bs + kMoveWarps - 1) / kMoveWarps, 2 * nl);
     k_commit_tree<<<grid, kMoveWarps * 32, 0, s>>>(p, bs);
   });
 }
