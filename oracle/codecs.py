@@ -101,8 +101,9 @@ def e4m3_encode(x, scale: float = 1.0) -> np.ndarray:
         return _bf16_table()[bits]
     flat = f.reshape(-1)
     out = np.empty(flat.shape, dtype=np.uint8)
-    # Encode the distinct values once (inputs are mostly bf16 values).
-    uniq, inv = np.unique(flat, return_inverse=True)
-    codes = np.array([e4m3_encode_scalar(v) for v in uniq], dtype=np.uint8)
+    # Encode the distinct values once (inputs are mostly bf16 values), told apart
+    # by their bits: the two zeros have codes of their own.
+    uniq, inv = np.unique(np.ascontiguousarray(flat).view(np.uint32), return_inverse=True)
+    codes = np.array([e4m3_encode_scalar(v) for v in uniq.view(np.float32)], dtype=np.uint8)
     out[:] = codes[inv]
     return out.reshape(f.shape)
