@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kMoveLayers = 64;    // layers per launch (the table is a kernel parameter)
 constexpr int kMoveWarps = 4;
+constexpr int64_t kCopyMoves = 1 << 24;   // moves per launch
 constexpr int kAhead = 8;          // loads in flight per warp; moves of a copying warp
 
 struct MoveLayer {
@@ -229,16 +230,20 @@ cudaError_t for_layers(const Ctx &c, MoveParams &P, F fn) {
 
 cudaError_t launch_copy_kv(Ctx &c, const int64_t *src, const int64_t *dst, int64_t n,
                            cudaStream_t s) {
-  if (n == 0) return cudaSuccess;
   MoveParams P{};
-  P.src = src;
-  P.dst = dst;
-  P.n = n;
-  return for_layers(c, P, [&](const MoveParams &p, int nl, int cols) {
-    const int64_t warps = (n + kAhead - 1) / kAhead * cols;
-    dim3 grid((unsigned)((warps + kMoveWarps - 1) / kMoveWarps), 2 * nl);
-    k_copy_kv<<<grid, kMoveWarps * 32, 0, s>>>(p, cols);
-  });
+  // A launch's moves keep its grid within 2^31 - 1 blocks whatever the row size.
+  for (int64_t i = 0; i < n; i += kCopyMoves) {
+    P.src = src + i;
+    P.dst = dst + i;
+    P.n = n - i < kCopyMoves ? n - i : kCopyMoves;
+    const cudaError_t e = for_layers(c, P, [&](const MoveParams &p, int nl, int cols) {
+      const int64_t warps = (p.n + kAhead - 1) / kAhead * cols;
+      dim3 grid((unsigned)((warps + kMoveWarps - 1) / kMoveWarps), 2 * nl);
+      k_copy_kv<<<grid, kMoveWarps * 32, 0, s>>>(p, cols);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_commit_tree(Ctx &c, int bs, const int32_t *rt, int64_t rt_stride,

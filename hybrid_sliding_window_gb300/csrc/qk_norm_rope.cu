@@ -11,11 +11,11 @@
 //
 // The pass should be bound by HBM: (Hq + 2 Hkv) D values read, Hq D + 2 Hkv D
 // written per token.  A token's query heads are contiguous (as are its key and
-// its value heads), so a persistent CTA - two per SM - streams whole tokens
+// its value heads), so a persistent CTA - four per SM - streams whole tokens
 // through a ring of shared-memory stages with bulk copies (one for each of q, k
 // and v, and the token's row of the angle table): a hundred KB in flight per SM
 // without a register for it.  A producer warp looks positions and slots up 32
-// units ahead; eight warps take the rows from shared memory.  A row is held by
+// units ahead; four warps take the rows from shared memory.  A row is held by
 // D / 8 lanes (bf16) or D / 4 (f32), each with two 8-byte words that hold the
 // two halves of its pairs: no value crosses lanes but the row's sum of squares.
 // With 1 / rms = rs the pair is
@@ -25,8 +25,9 @@
 // product with rs, two elements at a time (f32x2).
 // Measured: 32768 tokens of 64 + 8 + 8 heads, bf16 D = 128 (1.36 GB): 239 us, 5.7
 // TB/s (84 % of the copy peak; issue slots 65 % busy); 512 tokens of 64 + 4 + 4:
-// 6.4 us; 4099 tokens of 40 + 8 + 8, E4M3 pool: 26.4 us (the divisions by the
-// scale, and 6.7 tokens per CTA).
+// 6.2 us; 4099 tokens of 40 + 8 + 8, E4M3 pool: 26.0 us (6.7 tokens per CTA: the
+// start and the tail weigh; with products that enclose the quotient in place of
+// the divisions by the scale 25.7 us, not worth the second path).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

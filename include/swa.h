@@ -654,7 +654,8 @@ swa_status swa_tree_plan(swa_ctx *ctx, int32_t bs, const int32_t *parents,
  * tree, plan and ws are 16-byte aligned.  The tcgen05 kernel serves bf16 pools
  * with head_dim 64 or 128 and E4M3 pools with head_dim 128, at any page size
  * (16, 32 and 64 fastest); other configurations run the generic kernel, which
- * takes at most 65535 entries.  Both give the same bits from run to run.  Rows of entries that belong to no request are left as they are.
+ * takes at most 65535 entries.  Both give the same bits from run to run.  Rows
+ * of entries that belong to no request are left as they are.
  * `ws` as for swa_attn_decode (zero before its first use, reusable, also by
  * swa_attn_decode; calls that may overlap on the GPU need their own). */
 size_t swa_attn_tree_ws_bytes(const swa_ctx *ctx, int32_t layer, int32_t bs,
@@ -681,8 +682,8 @@ swa_status swa_attn_tree(swa_ctx *ctx, int32_t layer, int32_t bs,
  * stores them (E4M3: the float32 key is encoded without an intermediate
  * rounding).  q, k, v: rows of token t at t * *_stride elements, heads
  * contiguous (slices of one fused projection serve), f32 for an F32 pool, bf16
- * otherwise; rows, q_out and cos_sin 16-byte aligned.  q_out may be q itself when q_stride = Hq *
- * D.  q and q_out may be NULL (keys only), k and v may be NULL (queries only);
+ * otherwise; rows, q_out and cos_sin 16-byte aligned.  q_out may be q itself
+ * when q_stride = Hq * D.  q and q_out may be NULL (keys only), k and v may be NULL (queries only);
  * rot_dim 0 rotates nothing (positions, cos_sin unused); otherwise it is a
  * multiple of 16 up to D.  positions may be swa_tree_plan's.  A position
  * outside the table sets SWA_DEVERR_RANGE and leaves the token's outputs and

@@ -77,6 +77,19 @@ def test_copy(name):
     P.check_state()
 
 
+def test_long_copy_list():
+    """More entries than one launch takes, mostly padding; rows move at both ends."""
+    P = _pair("tiny")
+    grow(P, [1, 2], np.array([20, 20]))
+    n, src, dst = (1 << 24) + 9, P.ort[1, 15:20], P.ort[2, 15:20]
+    TR.move_rows(P.op, P.oa.mapping, zip(src, dst))
+    lists = torch.full((2, n), -1, dtype=torch.int64, device="cuda")
+    at = torch.tensor([0, 9, (1 << 24) - 1, 1 << 24, n - 1], device="cuda")
+    lists[0, at], lists[1, at] = dev(src), dev(dst)
+    api.swa_copy_kv(P.ctx, lists[0], lists[1])
+    P.check_state()
+
+
 def test_long_commit_in_batches():
     """A commit of more rows than a warp looks up at once, every one moving."""
     P = _pair("mimo", layers=[(OT.FULL, 0, 4), (OT.SLIDING, 300, 8)])

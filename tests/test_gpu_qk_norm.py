@@ -186,6 +186,31 @@ def test_same_bytes_as_store_kv():
                 assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -7, 1 / 448, 0.03, 1 / 3, 5.0, 1 + 2.0 ** -23, 2 - 2.0 ** -23,
+                                   0.3 * 2.0 ** -100, 1e30, 3e38, 1.2e-38, 1e-38, 1e-40, 2.0 ** -149])
+def test_e4m3_bytes_of_every_bf16_value(scale):
+    """Every bf16 pattern as K and as V: the bytes that swa_store_kv stores, and
+    the encoding of the float32 quotient."""
+    R = Run(4, 4, 128, "e4m3", n=(96, 32))
+    bits = np.random.default_rng(8).permutation(65536).astype(np.uint16).view(np.int16)
+    R.k = torch.tensor(bits, device="cuda").view(torch.bfloat16).reshape(R.n, 4, 128)
+    R.v = R.k.flip(0).contiguous()
+    R.P.k_scale, R.P.v_scale = scale, scale
+    api.swa_store_kv(R.P.ctx, 1, R.k, R.v, R.slots[0], R.slots[1], scale, scale)
+    want = [t.clone() for t in R.P.kv[1]]
+    for t in R.P.kv[1]:
+        t.zero_()
+    _call(R, 1, 0, weights=False)
+    rows = dev(R.P.last_alloc[0])
+    for x, t, w in zip((R.k, R.v), R.P.kv[1], want):
+        assert torch.equal(t.view(torch.uint8), w.view(torch.uint8))
+        x, got = x.float().cpu().numpy(), t[rows].view(torch.uint8).cpu().numpy().reshape(R.n, 4, 128)
+        ok = np.isfinite(x)
+        with np.errstate(all="ignore"):
+            codes = OC.e4m3_encode(np.clip(x[ok] / np.float32(scale), -1e30, 1e30).astype(np.float32), 1.0)
+        np.testing.assert_array_equal(got[ok], codes)
+
+
 def test_not_a_number_stays_in_its_row():
     R = Run(16, 4, 128, "bf16")
     table = _table(2048, 64)
