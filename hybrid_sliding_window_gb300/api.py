@@ -573,7 +573,7 @@ def _rows_ptr(t):
         return None, 0
     assert t.is_cuda, "device buffer expected"
     (n, heads, dim), (token, head, one) = t.shape, t.stride()
-    assert one == 1 and head == dim, "heads of a token must be contiguous"
+    assert one == 1 and (head == dim or heads == 1), "heads of a token must be contiguous"
     return t.data_ptr(), token if n > 1 else heads * dim
 
 
@@ -586,6 +586,7 @@ def swa_qk_norm_rope_store(ctx, layer, q, k, v, positions, full_loc, q_out, swa_
     kp, ks = _rows_ptr(k)
     vp, vs = _rows_ptr(v)
     n = (q if q is not None else k).shape[0]
+    assert k is None or v is None or k.shape[0] == v.shape[0] == n, "q, k and v of the same tokens"
     _check(lib().swa_qk_norm_rope_store(
         ctx.handle, layer, qp, qs, kp, ks, vp, vs, n, _ptr(positions), _ptr(q_weight),
         _ptr(k_weight), eps, _ptr(cos_sin), cos_sin.shape[0] if cos_sin is not None else 0, rot_dim,

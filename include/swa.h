@@ -708,9 +708,10 @@ swa_status swa_qk_norm_rope_store(swa_ctx *ctx, int32_t layer, const void *q,
  * columns prefix + accepted[j] to prefix + j, in both pools.  The slots and
  * req_to_token stay as they are; the request's length becomes prefix +
  * n_accepted[b], and the caller frees the pages wholly past it (swa_free).  A
- * list that is not strictly ascending, or reaches outside the row, sets
- * SWA_DEVERR_RANGE: nothing moves from the offending entry on.  Rows that
- * stay in place cost nothing. */
+ * request is named by one entry; entries with n_accepted 0 (padding) may repeat
+ * any.  A list that is not strictly ascending, or reaches outside the row, sets
+ * SWA_DEVERR_RANGE: nothing moves from the offending entry on.  Rows that stay
+ * in place cost nothing. */
 swa_status swa_commit_tree(swa_ctx *ctx, int32_t bs, const int32_t *req_to_token,
                            int64_t rt_stride, const int64_t *req_idx,
                            const int64_t *prefix_lens, const int32_t *accepted,
