@@ -23,7 +23,7 @@ __global__ void k_plan(const int32_t *rt, int64_t rt_stride, const int64_t *req_
   const int64_t first_q = pre ? pre[b] : hi;
   int64_t lo = first_q - lookback;
   if (lo < 0) lo = 0;
-  if (hi < 0) {
+  if (hi < lo) {   // no token, or no new token and a window of one: nothing is read
     if (threadIdx.x == 0) {
       hdr[b * 4 + 0] = 0; hdr[b * 4 + 1] = -1; hdr[b * 4 + 2] = 0; hdr[b * 4 + 3] = 0;
     }

@@ -52,6 +52,15 @@ def _trees(seed, sizes):
 
 
 # ------------------------------------------------------------------- plan ---
+@pytest.mark.parametrize("kind,window", [(OT.CHUNKED, 1), (OT.SLIDING, 0)])
+def test_request_without_nodes_where_a_token_sees_itself_only(kind, window):
+    """Its plan has no position at all: lo = prefix lies past its last token."""
+    P, S = _step(GPTOSS, 64, [200, 90, 128], [[-1, 0], [], []], layers=[(kind, window, 8), (OT.FULL, 0, 8)])
+    for layer in range(2):
+        S.check(layer)
+    assert api.swa_device_check(P.ctx) == 0
+
+
 @pytest.mark.parametrize("sizes", [[1], [8, 0, 3], [32, 33, 31, 64], [200, 1, 77], [1024, 5]])
 def test_plan_depths_positions_and_ancestors(sizes):
     P = _pair(TINY, 1, [5] * len(sizes), sizes)
