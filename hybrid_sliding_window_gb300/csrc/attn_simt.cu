@@ -445,6 +445,13 @@ SimtParams simt_params(const Ctx &c, const AttnArgs &a, const WsLayout &w) {
 
 template <bool kTree, int kGM, int kW>
 cudaError_t launch_simt(const Ctx &c, const SimtParams &P, const AttnArgs &a, cudaStream_t s) {
+  // With more rows than max_batch the tickets reach past the context's common
+  // ticket block, to where calls of fewer rows keep their partials: whatever
+  // those left there is cleared.
+  if (a.nq > c.cfg.max_batch && P.max_splits > 1) {
+    const cudaError_t e = cudaMemsetAsync(P.tickets, 0, (size_t)a.nq * P.hkv * sizeof(int32_t), s);
+    if (e != cudaSuccess) return e;
+  }
   dim3 grid(P.max_splits, P.hkv, a.nq);
   if (c.cfg.kv_dtype == SWA_DTYPE_F32) return dispatch_dl<float, float, kTree, kGM, kW>(P.D, grid, P, s);
   if (c.cfg.kv_dtype == SWA_DTYPE_BF16)

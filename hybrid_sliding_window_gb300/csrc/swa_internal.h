@@ -112,7 +112,9 @@ struct Ctx {
 // one size for every layer and every decode batch of a context (max(nq,
 // max_batch) x the largest KV-head count, int32), so decode calls of any
 // layers can share one workspace: the partials of one layer never cover the
-// tickets of another, which are zero between launches.
+// tickets of another, which are zero between launches.  Calls of more rows
+// (extend and tree attention on the generic kernel) clear their tickets before
+// they launch, and leave the common block zero.
 inline size_t ws_tickets_bytes(const Ctx &c, int64_t nq) {
   int hmax = 1;
   for (const LayerInfo &L : c.layers) hmax = L.hkv > hmax ? L.hkv : hmax;

@@ -514,9 +514,10 @@ swa_status swa_plan(swa_ctx *ctx, int32_t bs, const int32_t *req_to_token,
  * launch; `ws` is the split workspace (size from *_ws_bytes) and must be
  * zero-filled before its first use (the kernels leave it reusable).  Its
  * layout is [256 B counters][tickets][partials] with a ticket block of one
- * size per context for batches up to max_batch, so decode calls of any
- * layers may share one workspace sized for the largest of them; a generic-
- * path extend call with more query tokens than max_batch needs its own.
+ * size per context for batches up to max_batch, so calls of any layers may
+ * share one workspace sized for the largest of them (a generic-path extend or
+ * tree call with more rows than max_batch clears its own, longer ticket block
+ * on the stream first).
  *
  * swa_attn_decode: one query per request at p = seq_lens[b] - 1 (its KV
  * already stored). max_seq_len bounds seq_lens (host; sizes the grid).  On
@@ -656,8 +657,9 @@ swa_status swa_tree_plan(swa_ctx *ctx, int32_t bs, const int32_t *parents,
  * (16, 32 and 64 fastest); other configurations run the generic kernel, which
  * takes at most 65535 entries.  Both give the same bits from run to run.  Rows
  * of entries that belong to no request are left as they are.
- * `ws` as for swa_attn_decode (zero before its first use, reusable, also by
- * swa_attn_decode; calls that may overlap on the GPU need their own). */
+ * `ws` as for swa_attn_decode (zero before its first use, then reusable by
+ * calls of any size and by the other attention families; calls that may overlap
+ * on the GPU need their own). */
 size_t swa_attn_tree_ws_bytes(const swa_ctx *ctx, int32_t layer, int32_t bs,
                               int64_t n_tokens, int32_t max_new,
                               int32_t max_seq_len);

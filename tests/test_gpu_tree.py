@@ -411,6 +411,62 @@ def test_workspace_shared_with_decode_and_across_kernels(shape):
     assert api.swa_device_check(P.ctx) == 0
 
 
+@pytest.mark.parametrize("shape", [TINY, MIMO, dict(LLAMA4, D=64)], ids=["tiny", "mimo", "e4m3-d64"])
+def test_workspace_reused_by_calls_of_other_sizes(shape):
+    """One workspace, zeroed once, under generic-kernel tree and extend calls
+    whose rows - more than max_batch of them - rise and fall, with decode calls
+    between: outputs as with fresh ones."""
+    ps = 1 if shape is TINY else 64
+    P, S = _step(shape, ps, [900, 333], _trees(23, [260, 130]), 0)
+    rows, pre, seq = S.d["rows"], S.d["pre"], S.d["seq"]
+    assert P.ctx.cfg.max_batch == 64
+    dplan = torch.zeros(api.swa_plan_bytes(P.ctx, 2, 1), dtype=torch.uint8, device="cuda")
+    api.swa_plan(P.ctx, P.rt, rows, None, seq, dplan, 1)
+    qs = [P.to_dev(S.queries(l)) for l in range(2)]
+    size = max([api.swa_attn_extend_ws_bytes(P.ctx, l, S.n, S.max_seq) for l in range(2)]
+               + [S.workspace(l).numel() for l in range(2)])
+
+    def tree_call(l, sizes, ws, chain):
+        """The first nodes of each tree (with the parents' smaller indices, trees again)."""
+        at = np.concatenate([np.arange(a, a + k) for a, k in zip(S.indptr, sizes)])
+        n, indptr = int(sum(sizes)), dev(np.concatenate([[0], np.cumsum(sizes)]))
+        q = qs[l][dev(at)].contiguous()
+        out = torch.full_like(q, 7.0)
+        end = pre + dev(sizes)
+        plan = torch.zeros(api.swa_plan_bytes(P.ctx, 2, 260), dtype=torch.uint8, device="cuda")
+        api.swa_plan(P.ctx, P.rt, rows, pre, end, plan, 260)
+        if chain:
+            api.swa_attn_extend(P.ctx, l, P.rt, rows, pre, end, indptr, n, 260, S.max_seq, plan, q, P.sinks_d[l],
+                                P.scale, out, ws, P.k_scale, P.v_scale)
+            return out
+        tree = torch.zeros(api.swa_tree_bytes(P.ctx, n, 260), dtype=torch.uint8, device="cuda")
+        api.swa_tree_plan(P.ctx, S.d["parents"][dev(at)].contiguous(), pre, indptr, n, 260, tree)
+        api.swa_attn_tree(P.ctx, l, P.rt, rows, pre, indptr, n, 260, S.max_seq, plan, tree, q, P.sinks_d[l],
+                          P.scale, out, ws, P.k_scale, P.v_scale)
+        return out
+
+    def decode_call(l, ws):
+        out = torch.full_like(qs[l][:2], 7.0)
+        api.swa_attn_decode(P.ctx, l, P.rt, rows, seq, S.max_seq, dplan, qs[l][:2].contiguous(), P.sinks_d[l],
+                            P.scale, out, ws, P.k_scale, P.v_scale)
+        return out
+
+    def run(ws):
+        got = []
+        for sizes in ([70, 9], [260, 130], [30, 40], [200, 130], [3, 2], [260, 1]):
+            for l in (1, 0):
+                for chain in (False, True):
+                    got.append(tree_call(l, sizes, ws(), chain))
+                    got.append(decode_call(l, ws()))
+        return got
+
+    shared = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    want = run(lambda: torch.zeros(size, dtype=torch.uint8, device="cuda"))
+    for i, (a, b) in enumerate(zip(run(lambda: shared), want)):
+        assert torch.equal(a, b), f"call {i}"
+    assert api.swa_device_check(P.ctx) == 0
+
+
 # ---------------------------------------------------------------- refusals ---
 def test_refusals_leave_the_context_usable():
     P, S = _step(MIMO, 64, [100, 30], _trees(16, [5, 9]))
