@@ -772,7 +772,6 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
               advance(vs, vp, ++vt == n - 1 ? 1 : 2);
             }
             if (u + 2 >= U) tc_commit(bar(B_ODONE + g));
-            if (U == 1) tc_commit(bar(B_ODONE + 1));
           }
           if (u + 2 < U) {                   // S(u + 2), of the same group
             if (fresh && !(ok = mbar_wait_ready(bar(B_FULL + ks), kp, &s_abort))) break;
@@ -812,6 +811,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
     const float sc = P.scale_log2;
     const uint64_t sc2 = f2pack(sc, sc);
     int steps = 0, joins = 0;
+    int both = 0;                            // segments in which both groups have a step
     // A segment as this row sees it, with what it loads of its node: taken from
     // the ring before the previous segment's epilogue, which covers the loads.
     struct Mine {
@@ -1020,7 +1020,13 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
       if (!alive || !take(nd + 1, next)) break;
       if (warming) continue;
       // ---- epilogue ----
-      if (!wait_all(bar(B_ODONE + grp), nd & 1)) break;
+      // A segment of one step is group 0's: group 1's O is not written, and its
+      // barrier has no phase (one that completed without a step of group 1 could
+      // complete before group 1 has seen the phase before it, whose parity would
+      // then be gone).
+      const bool one_step = !alone && n_tiles == 1;
+      const uint32_t done0 = nd & 1, done1 = both & 1;   // phases of the two O
+      if (!(grp && one_step) && !wait_all(bar(B_ODONE + grp), grp ? done1 : done0)) break;
       float w0 = 1.f, w1 = 0.f;              // weights of this group's and the other's O
       if (!alone) {
         // Join the groups' halves of the keys: row statistics through shared
@@ -1028,7 +1034,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
         s_stat[grp * kTileRows + r] = make_float2(m_run, l_run);
         mbar_arrive(bar(B_STAT));
         if (!wait_all(bar(B_STAT), joins & 1)) break;
-        if (!wait_all(bar(B_ODONE + (grp ^ 1)), nd & 1)) break;
+        if ((grp || !one_step) && !wait_all(bar(B_ODONE + (grp ^ 1)), grp ? done0 : done1)) break;
         const float2 o = s_stat[(grp ^ 1) * kTileRows + r];
         const float m = fmaxf(m_run, o.x);
         w0 = m_run == -INFINITY ? 0.f : exp2f(m_run - m);
@@ -1116,6 +1122,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
         tc_fence_after();
         ++joins;
       }
+      both += !one_step;
     }
   }
   if (kGather) asm volatile("cp.async.wait_all;\n" ::: "memory");

@@ -467,6 +467,28 @@ def test_workspace_reused_by_calls_of_other_sizes(shape):
     assert api.swa_device_check(P.ctx) == 0
 
 
+@pytest.mark.parametrize("shape", [MIMO, LLAMA4], ids=["mimo", "llama4"])
+def test_one_tile_items_behind_pairs_and_wide_items(shape):
+    """CTAs whose last item has one key tile, behind a pair of items (whole items)
+    or an item of two Q tiles (stretches): many launches, always the same bits."""
+    n = 57                                  # three items for each of 19 CTAs of a KV head
+    sizes = [12 if b % 3 == 0 else 3 for b in range(n)]
+    P, S = _step(shape, 64, [20 + b for b in range(n)], _trees(25, sizes))
+    for l in range(2):
+        S.check(l, requests=[0, 1, 2, 27, 55, 56], what="one tile")
+        q = P.to_dev(S.queries(l))
+        for bound in (S.max_seq, 8192):
+            S.max_seq = bound
+            ws, want = S.workspace(l), torch.empty_like(q)
+            S.run(l, q, want, ws)
+            out = torch.empty_like(q)
+            for _ in range(300):
+                S.run(l, q, out, ws)
+            assert torch.equal(out, want)
+        S.max_seq = int(S.seq.max())
+    assert api.swa_device_check(P.ctx) == 0
+
+
 # ---------------------------------------------------------------- refusals ---
 def test_refusals_leave_the_context_usable():
     P, S = _step(MIMO, 64, [100, 30], _trees(16, [5, 9]))
