@@ -893,9 +893,10 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
           if (any_edge) {
             if (row_valid || warming) {
               allow = bit_range(lo_row - c0, behind - c0);
+              // (The warm-up must not read the tree: it may still be written.)
               if (c0 + 64 > behind)
-                allow |= (few ? shift_bits(above, c0 - behind)
-                              : row_bits(row, P.tree.words, c0 - behind)) &
+                allow |= (few || warming ? shift_bits(above, c0 - behind)
+                                         : row_bits(row, P.tree.words, c0 - behind)) &
                          bit_range(max(lo_row, behind) - c0, 64);
             }
             if (!__any_sync(0xffffffffu, allow != 0ull)) {

@@ -489,6 +489,30 @@ def test_one_tile_items_behind_pairs_and_wide_items(shape):
     assert api.swa_device_check(P.ctx) == 0
 
 
+@pytest.mark.parametrize("shape,nodes", [(MIMO, 65), (MIMO, 300), (LLAMA4, 130)], ids=["mimo-65", "mimo-300", "llama4-130"])
+def test_captured_step_of_wide_trees_with_changing_parents(shape, nodes):
+    """Plan and attention captured back to back, trees of more nodes than a
+    register holds: every replay attends the parents that are there then."""
+    rng = np.random.default_rng(26)
+    P, S = _step(shape, 64, [150, 60], [random_parents(rng, nodes), random_parents(rng, 20)])
+    qs = [P.to_dev(S.queries(l)) for l in range(2)]
+    outs, wss = [torch.empty_like(q) for q in qs], [S.workspace(l) for l in range(2)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for l in range(2):
+            S.make_plans()
+            S.run(l, qs[l], outs[l], wss[l])
+    for roots in (0.1, 1.0, 0.5):
+        S.parents = [random_parents(rng, nodes, roots), random_parents(rng, 20, roots)]
+        S.d["parents"].copy_(dev([p for t in S.parents for p in t], torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        for l in range(2):
+            at, ref, mag = S.oracle(l, S.queries(l))
+            assert_attention(outs[l].float().cpu().numpy()[at], ref, mag, P.dtype, f"roots {roots} layer {l}")
+    assert api.swa_device_check(P.ctx) == 0
+
+
 # ---------------------------------------------------------------- refusals ---
 def test_refusals_leave_the_context_usable():
     P, S = _step(MIMO, 64, [100, 30], _trees(16, [5, 9]))
