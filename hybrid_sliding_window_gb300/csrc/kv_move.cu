@@ -52,7 +52,9 @@ struct MoveParams {
 };
 
 // Rows of the move (full slots a -> b) in the layer's pool; false: nothing to
-// move there.
+// move there.  A copy's source may have left the window (kNode false); a node of
+// this step has its SWA slot, or the tables are broken.
+template <bool kNode>
 __device__ __forceinline__ bool move_rows(const MoveParams &P, const MoveLayer &L, int64_t a,
                                           int64_t b, int64_t &ra, int64_t &rb) {
   if (a < 0 || b < 0 || a >= P.rows_full || b >= P.rows_full) {
@@ -62,8 +64,8 @@ __device__ __forceinline__ bool move_rows(const MoveParams &P, const MoveLayer &
   if (!L.in_full) {
     a = P.mapping[a];
     b = P.mapping[b];
-    if (a <= 0) return false;          // the source left the window: full layers only
-    if (b <= 0) {
+    if (!kNode && a <= 0) return false;   // full layers only
+    if (a <= 0 || b <= 0) {
       set_error(P.err, SWA_DEVERR_WINDOW_EVICTED);
       return false;
     }
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
   bool live = false;
   if (lane < kAhead && i < P.n) {
     const int64_t a = P.src[i], b = P.dst[i];
-    live = a != -1 && b != -1 && move_rows(P, L, a, b, ra, rb);
+    live = a != -1 && b != -1 && move_rows<false>(P, L, a, b, ra, rb);
   }
   run_moves((blockIdx.y & 1) ? L.v : L.k, col, col < L.row_bytes, live, ra, rb);
 }
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32)
     const unsigned wrong = __ballot_sync(0xffffffffu, bad);
     int64_t ra = 0, rb = 0;
     bool live = j < n && (!wrong || lane < __ffs(wrong) - 1) && a != j;
-    if (live) live = move_rows(P, L, row[pre + a], row[pre + j], ra, rb);
+    if (live) live = move_rows<true>(P, L, row[pre + a], row[pre + j], ra, rb);
     run_row_moves((blockIdx.y & 1) ? L.v : L.k, L.row_bytes, lane, live, ra, rb);
     if (wrong) {
       set_error(P.err, SWA_DEVERR_RANGE);

@@ -81,7 +81,7 @@ enum swa_layout { SWA_LAYOUT_PER_LAYER = 0, SWA_LAYOUT_ENVELOPE = 1 };
 
 /* Error-word bits set by device-side checks. */
 enum swa_device_error {
-  SWA_DEVERR_WINDOW_EVICTED = 1,  /* an attended key's SWA mapping was 0        */
+  SWA_DEVERR_WINDOW_EVICTED = 1,  /* an attended or moved row's SWA mapping was 0 */
   SWA_DEVERR_COUNT = 2,           /* freed page count differs from host count  */
   SWA_DEVERR_RANGE = 4,           /* slot / page / position out of range       */
   SWA_DEVERR_TIMEOUT = 8          /* a kernel gave up a bounded wait (its
@@ -712,8 +712,9 @@ swa_status swa_qk_norm_rope_store(swa_ctx *ctx, int32_t layer, const void *q,
  * n_accepted[b], and the caller frees the pages wholly past it (swa_free).  A
  * request is named by one entry; entries with n_accepted 0 (padding) may repeat
  * any.  A list that is not strictly ascending, or reaches outside the row, sets
- * SWA_DEVERR_RANGE: nothing moves from the offending entry on.  Rows that stay
- * in place cost nothing. */
+ * SWA_DEVERR_RANGE: nothing moves from the offending entry on.  A move whose
+ * source or destination has no SWA slot sets SWA_DEVERR_WINDOW_EVICTED and is
+ * made on full layers only.  Rows that stay in place cost nothing. */
 swa_status swa_commit_tree(swa_ctx *ctx, int32_t bs, const int32_t *req_to_token,
                            int64_t rt_stride, const int64_t *req_idx,
                            const int64_t *prefix_lens, const int32_t *accepted,

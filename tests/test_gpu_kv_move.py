@@ -129,6 +129,32 @@ def test_device_checks():
     assert api.swa_device_check(P.ctx) == api.SWA_DEVERR_WINDOW_EVICTED
 
 
+@pytest.mark.parametrize("name", ["mimo", "envelope", "ring"])
+def test_commit_of_a_node_without_its_swa_slot(name):
+    """An accepted node whose SWA slot is missing (a table that is broken: the
+    nodes of a step have both slots) is flagged; its row moves on full layers
+    only, and the other nodes' on every layer."""
+    P = _pair(name)
+    pre = np.array([40, 30])
+    grow(P, [1, 2], pre)
+    P.extend([1, 2], pre, pre + 20)
+    lost = int(P.ort[1, 40 + 6])
+    P.oa.mapping[lost] = 0
+    P.ctx.mapping()[lost] = 0
+    acc = [[2, 6, 9], [5, 7, 8]]
+    for b in range(2):
+        TR.commit(P.op, P.oa.mapping, P.ort[b + 1], int(pre[b]), acc[b])
+    api.swa_commit_tree(P.ctx, P.rt, dev([1, 2]), dev(pre), dev(acc, torch.int32), dev([3, 3], torch.int32))
+    assert api.swa_device_check(P.ctx) == api.SWA_DEVERR_WINDOW_EVICTED
+    P.check_state()
+    # a copy takes such a source on full layers without a flag
+    src, dst = [lost], [int(P.ort[2, 31])]
+    TR.move_rows(P.op, P.oa.mapping, zip(src, dst))
+    api.swa_copy_kv(P.ctx, dev(src), dev(dst))
+    assert api.swa_device_check(P.ctx) == 0
+    P.check_state()
+
+
 def test_refusals():
     P = _pair("mimo")
     L, h = api.lib(), P.ctx.handle
