@@ -37,8 +37,7 @@ struct MoveParams {
   MoveLayer layer[kMoveLayers];
   int32_t ps;
   int64_t rows_full, rows_swa;   // slots of each pool, padding page included
-  const int64_t *mapping;
-  int64_t map_len;
+  const int64_t *mapping;        // longer than rows_full
   int32_t *err;
   // copy
   const int64_t *src, *dst;
@@ -209,7 +208,6 @@ cudaError_t for_layers(const Ctx &c, MoveParams &P, F fn) {
   P.rows_full = c.cfg.size_full + c.cfg.page_size;
   P.rows_swa = c.cfg.size_swa + c.cfg.page_size;
   P.mapping = c.mapping;
-  P.map_len = c.mapping_len;
   P.err = c.err_word;
   const int total = (int)c.layers.size();
   for (int l0 = 0; l0 < total; l0 += kMoveLayers) {
