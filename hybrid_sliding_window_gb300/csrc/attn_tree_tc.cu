@@ -1050,7 +1050,7 @@ __global__ void __launch_bounds__(TreeGeo<kD, kF8>::kThreads, 1)
         const float mfin = fmaxf(mr, sg2);
         const float rsc = exp2f(mr - mfin);
         const float denom = l_run * rsc + (P.sinks ? exp2f(sg2 - mfin) : 0.f);
-        f = denom > 0.f ? rsc / denom * P.v_scale : 0.f;
+        f = rsc / denom * P.v_scale;         // (no row is without a key: it attends itself)
       }
       w0 *= f;
       w1 *= f;

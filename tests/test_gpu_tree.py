@@ -513,6 +513,34 @@ def test_captured_step_of_wide_trees_with_changing_parents(shape, nodes):
     assert api.swa_device_check(P.ctx) == 0
 
 
+@pytest.mark.parametrize("path", [-1, 0])
+@pytest.mark.parametrize("shape", [MIMO, GPTOSS, LLAMA4], ids=["mimo", "gptoss", "llama4"])
+def test_not_a_number_stays_in_its_row(shape, path):
+    """A query that is not a number gives an output that is not a number, on
+    items whose keys one group of rows takes, that two share, and that are split
+    over the GPU; every other row keeps its bits."""
+    P, S = _step(shape, 64, [300, 700, 20], _trees(24, [9, 20, 1]), path)
+    for l in range(2):
+        q = P.to_dev(S.queries(l))
+        hurt = q.clone()
+        at = [0, 4, 9 + 17, 9 + 20]
+        for i, r in enumerate(at):
+            hurt[r, 3 * i, 5] = float("nan")
+        for bound in (S.max_seq, 8192):
+            S.max_seq = bound
+            out, bad = torch.empty_like(q), torch.empty_like(q)
+            S.run(l, q, out, S.workspace(l))
+            S.run(l, hurt, bad, S.workspace(l))
+            is_bad = torch.isnan(bad)
+            for i, r in enumerate(at):
+                assert is_bad[r, 3 * i].all(), f"layer {l} row {r}"
+                is_bad[r, 3 * i] = False
+                out[r, 3 * i] = bad[r, 3 * i] = 0
+            assert not is_bad.any() and torch.equal(out, bad)
+        S.max_seq = int(S.seq.max())
+    assert api.swa_device_check(P.ctx) == 0
+
+
 # ---------------------------------------------------------------- refusals ---
 def test_refusals_leave_the_context_usable():
     P, S = _step(MIMO, 64, [100, 30], _trees(16, [5, 9]))
