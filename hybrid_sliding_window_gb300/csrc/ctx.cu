@@ -808,6 +808,10 @@ swa_status swa_attn_tree(swa_ctx *c, int32_t layer, int32_t bs, const int32_t *r
   const bool tc = use_tree_tc(c, layer);
   if (n_tokens > (tc ? 0x7fffffff : 65535))
     return fail(c, SWA_ERR_INVALID, "n_tokens > 65535 on the generic path");
+  // That kernel scales after it has masked: a masked score of -inf must stay one.
+  const float scale = c->cfg.kv_dtype == SWA_DTYPE_E4M3 ? sm_scale * k_scale : sm_scale;
+  if (tc && !(scale > 0 && std::isfinite(scale)))
+    return fail(c, SWA_ERR_INVALID, "the tcgen05 path needs a positive, finite sm_scale (x k_scale)");
   swa::AttnArgs a{};
   a.layer = layer;
   a.nq = (int)n_tokens;

@@ -586,6 +586,30 @@ def test_refusals_leave_the_context_usable():
     S.check(1, what="after refusals")
 
 
+@pytest.mark.parametrize("shape", [MIMO, LLAMA4], ids=["mimo", "llama4"])
+def test_scales_that_a_masked_score_does_not_survive(shape):
+    """-inf times a scale that is not positive is no -inf: refused where the
+    kernel scales after masking, served by the generic kernel."""
+    P, S = _step(shape, 64, [100, 30], _trees(27, [5, 9]))
+    q = P.to_dev(S.queries(1))
+    out = torch.full_like(q, 7.0)
+    ws = S.workspace(1)
+    good = P.scale
+    for bad in (0.0, -good, float("nan"), float("inf")):
+        P.scale = bad
+        with pytest.raises(api.SwaError) as e:
+            S.run(1, q, out, ws)
+        assert e.value.status == api.SWA_ERR_INVALID
+    assert (out == 7).all()
+    api.swa_set_attn_path(P.ctx, 0)
+    for P.scale in (0.0, -good):
+        S.check(1, what=f"scale {P.scale}")
+    P.scale = good
+    api.swa_set_attn_path(P.ctx, -1)
+    S.check(1)
+    assert api.swa_device_check(P.ctx) == 0
+
+
 def test_device_checks():
     """Columns past the req_to_token row, and an evicted key in the window."""
     P, S = _step(MIMO, 64, [700, 30], _trees(17, [5, 9]))
