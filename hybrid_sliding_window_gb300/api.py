@@ -225,12 +225,16 @@ class SwaCtx:
         self.cfg = cfg
         self._layers_arr = arr
         self.layers = layers
+        # what the calls' arguments are compared with
+        self.io_dtype = torch.float32 if kv_dtype == DTYPE_F32 else torch.bfloat16
+        self.num_q_heads, self.head_dim = num_q_heads, head_dim
         self.full_envelope = full_envelope
         self.swa_envelope = swa_envelope
         nbytes = lib().swa_state_bytes(C.byref(cfg))
         if nbytes == 0:
             raise SwaError(SWA_ERR_INVALID, "swa_state_bytes rejected the config")
         self.state = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.gpu = self.state.get_device()
         handle = C.c_void_p()
         st = lib().swa_ctx_create(C.byref(cfg), _ptr(self.state), _ptr(init_free_full),
                                   _ptr(init_free_swa), _stream(stream), C.byref(handle))
@@ -536,7 +540,45 @@ def swa_attn_extend(ctx, layer, req_to_token, req_idx, prefix_lens, seq_lens, qo
 
 
 # ------------------------------------------------------- speculative step ---
+# These calls take a model's own tensors (norm weights, angle tables, slices of a
+# projection): what a kernel would read or write by a raw pointer is compared with
+# what it takes there first.
 TREE_MAX_NODES = 1024
+
+
+def _refuse(msg):
+    raise SwaError(SWA_ERR_INVALID, msg)
+
+
+def _arg(t, what, dtype, n, ctx):
+    """Pointer to at least n contiguous elements of the type on the context's GPU
+    (None stays NULL, which the library refuses where it needs the argument)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or t.get_device() != ctx.gpu:
+        _refuse(f"{what}: {n} or more contiguous {dtype} on GPU {ctx.gpu} expected, "
+                f"not {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _vector(t, what, n, ctx):
+    """A model's own vector of n floats, or None."""
+    if t is not None and t.numel() != n:
+        _refuse(f"{what}: {n} values expected, not {tuple(t.shape)}")
+    return _arg(t, what, torch.float32, n, ctx)
+
+
+def _kv_heads(ctx, layer):
+    if not 0 <= layer < len(ctx.layers):
+        _refuse("layer out of range")
+    return ctx.layers[layer]["num_kv_heads"]
+
+
+def _table(rt, ctx):
+    """req_to_token: (pointer, row length)."""
+    if rt.ndim != 2:
+        _refuse("req_to_token: [rows, columns] expected")
+    return _arg(rt, "req_to_token", torch.int32, 0, ctx), rt.shape[1]
 
 
 def swa_tree_bytes(ctx, n_tokens, max_new):
@@ -546,9 +588,14 @@ def swa_tree_bytes(ctx, n_tokens, max_new):
 def swa_tree_plan(ctx, parents, prefix_lens, qo_indptr, n_tokens, max_new, tree, positions=None,
                   stream=None):
     """Depths, positions and ancestor sets of the batch's drafted nodes."""
-    _check(lib().swa_tree_plan(ctx.handle, prefix_lens.numel(), _ptr(parents), _ptr(prefix_lens),
-                               _ptr(qo_indptr), n_tokens, max_new, _ptr(positions), _ptr(tree),
-                               tree.numel(), _stream(stream)), ctx.handle)
+    bs = prefix_lens.numel()
+    i64 = torch.int64
+    _check(lib().swa_tree_plan(ctx.handle, bs, _arg(parents, "parents", torch.int32, n_tokens, ctx),
+                               _arg(prefix_lens, "prefix_lens", i64, bs, ctx),
+                               _arg(qo_indptr, "qo_indptr", i64, bs + 1, ctx), n_tokens, max_new,
+                               _arg(positions, "positions", i64, n_tokens, ctx),
+                               _arg(tree, "tree", torch.uint8, 0, ctx), tree.numel(),
+                               _stream(stream)), ctx.handle)
 
 
 def swa_attn_tree_ws_bytes(ctx, layer, bs, n_tokens, max_new, max_seq_len):
@@ -558,23 +605,37 @@ def swa_attn_tree_ws_bytes(ctx, layer, bs, n_tokens, max_new, max_seq_len):
 def swa_attn_tree(ctx, layer, req_to_token, req_idx, prefix_lens, qo_indptr, n_tokens, max_new,
                   max_seq_len, plan, tree, q, sinks, sm_scale, out, ws, k_scale=1.0, v_scale=1.0,
                   stream=None):
+    L, h = lib(), ctx.handle
     bs = prefix_lens.numel()
-    stride = req_to_token.shape[1] if req_to_token is not None else 0
-    _check(lib().swa_attn_tree(ctx.handle, layer, bs, _ptr(req_to_token), stride, _ptr(req_idx),
-                               _ptr(prefix_lens), _ptr(qo_indptr), n_tokens, max_new, max_seq_len,
-                               _ptr(plan), _ptr(tree), _ptr(q), _ptr(sinks), sm_scale, k_scale,
-                               v_scale, _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
-           ctx.handle)
+    _kv_heads(ctx, layer)
+    hq, i64, u8 = ctx.num_q_heads, torch.int64, torch.uint8
+    rt, stride = _table(req_to_token, ctx) if req_to_token is not None else (None, 0)
+    full = ctx.layers[layer]["kind"] == LAYER_FULL
+    rows = n_tokens * hq * ctx.head_dim
+    _check(L.swa_attn_tree(
+        h, layer, bs, rt, stride, _arg(req_idx, "req_idx", i64, bs, ctx),
+        _arg(prefix_lens, "prefix_lens", i64, bs, ctx), _arg(qo_indptr, "qo_indptr", i64, bs + 1, ctx),
+        n_tokens, max_new, max_seq_len,
+        _arg(plan, "plan", u8, 0 if full else L.swa_plan_bytes(h, bs, max_new), ctx),
+        _arg(tree, "tree", u8, L.swa_tree_bytes(h, n_tokens, max_new), ctx),
+        _arg(q, "q", ctx.io_dtype, rows, ctx), _vector(sinks, "sinks", hq, ctx), sm_scale,
+        k_scale, v_scale, _arg(out, "out", ctx.io_dtype, rows, ctx), _arg(ws, "ws", u8, 0, ctx),
+        ws.numel(), _stream(stream)), h)
 
 
-def _rows_ptr(t):
-    """[n, heads, D] rows that may be strided over tokens -> (pointer, elements between tokens)."""
+def _rows(t, what, ctx, heads):
+    """[n, heads, D] rows that may be strided over tokens -> (pointer, elements
+    between tokens, n); of an absent part (NULL, 0, -1)."""
     if t is None:
-        return None, 0
-    assert t.is_cuda, "device buffer expected"
-    (n, heads, dim), (token, head, one) = t.shape, t.stride()
-    assert one == 1 and (head == dim or heads == 1), "heads of a token must be contiguous"
-    return t.data_ptr(), token if n > 1 else heads * dim
+        return None, 0, -1
+    shape, strides = t.shape, t.stride()
+    dim = ctx.head_dim
+    if (len(shape) != 3 or shape[1] != heads or shape[2] != dim or t.dtype is not ctx.io_dtype
+            or strides[2] != 1 or (strides[1] != dim and heads > 1) or t.get_device() != ctx.gpu):
+        _refuse(f"{what}: [tokens, {heads}, {dim}] {ctx.io_dtype} on GPU {ctx.gpu} expected, the heads of a "
+                f"token contiguous, not {tuple(shape)} {t.dtype} on {t.device} with strides {strides}")
+    n = shape[0]
+    return t.data_ptr(), strides[0] if n > 1 else heads * dim, n
 
 
 def swa_qk_norm_rope_store(ctx, layer, q, k, v, positions, full_loc, q_out, swa_loc=None,
@@ -582,30 +643,51 @@ def swa_qk_norm_rope_store(ctx, layer, q, k, v, positions, full_loc, q_out, swa_
                            interleaved=False, k_scale=1.0, v_scale=1.0, stream=None):
     """q, k, v: [n, heads, D], possibly slices of one fused projection; any of
     q (with q_out) or k and v may be None."""
-    qp, qs = _rows_ptr(q)
-    kp, ks = _rows_ptr(k)
-    vp, vs = _rows_ptr(v)
-    n = (q if q is not None else k).shape[0]
-    assert k is None or v is None or k.shape[0] == v.shape[0] == n, "q, k and v of the same tokens"
+    hkv, d = _kv_heads(ctx, layer), ctx.head_dim
+    qp, qs, nq = _rows(q, "q", ctx, ctx.num_q_heads)
+    kp, ks, nk = _rows(k, "k", ctx, hkv)
+    vp, vs, nv = _rows(v, "v", ctx, hkv)
+    n = max(nq, nk, nv)
+    if n < 0 or (nq >= 0 and nq != n) or (nk >= 0 and nk != n) or (nv >= 0 and nv != n):
+        _refuse("q, k and v of the same tokens expected")
+    i64 = torch.int64
+    max_pos = 0
+    if rot_dim > 0 and cos_sin is not None:
+        shape = cos_sin.shape
+        if len(shape) != 2 or shape[1] != rot_dim:
+            _refuse(f"cos_sin: [positions, {rot_dim}] expected, not {tuple(shape)}")
+        max_pos = shape[0]
     _check(lib().swa_qk_norm_rope_store(
-        ctx.handle, layer, qp, qs, kp, ks, vp, vs, n, _ptr(positions), _ptr(q_weight),
-        _ptr(k_weight), eps, _ptr(cos_sin), cos_sin.shape[0] if cos_sin is not None else 0, rot_dim,
-        1 if interleaved else 0, _ptr(full_loc), _ptr(swa_loc), k_scale, v_scale, _ptr(q_out),
+        ctx.handle, layer, qp, qs, kp, ks, vp, vs, n,
+        _arg(positions, "positions", i64, n if rot_dim > 0 else 0, ctx),
+        _vector(q_weight, "q_weight", d, ctx), _vector(k_weight, "k_weight", d, ctx), eps,
+        _arg(cos_sin, "cos_sin", torch.float32, 0, ctx), max_pos, rot_dim, 1 if interleaved else 0,
+        _arg(full_loc, "full_loc", i64, nk, ctx), _arg(swa_loc, "swa_loc", i64, nk, ctx), k_scale,
+        v_scale, _arg(q_out, "q_out", ctx.io_dtype, nq * ctx.num_q_heads * d, ctx),
         _stream(stream)), ctx.handle)
 
 
 def swa_commit_tree(ctx, req_to_token, req_idx, prefix_lens, accepted, n_accepted, stream=None):
     """accepted: [bs, max_accept] int32 node indices, ascending; n_accepted: [bs] int32."""
-    _check(lib().swa_commit_tree(ctx.handle, prefix_lens.numel(), _ptr(req_to_token),
-                                 req_to_token.shape[1], _ptr(req_idx), _ptr(prefix_lens),
-                                 _ptr(accepted), accepted.shape[1], _ptr(n_accepted),
-                                 _stream(stream)), ctx.handle)
+    bs, i32, i64 = prefix_lens.numel(), torch.int32, torch.int64
+    rt, stride = _table(req_to_token, ctx)
+    if accepted.ndim != 2:
+        _refuse("accepted: [requests, nodes] expected")
+    m = accepted.shape[1]
+    _check(lib().swa_commit_tree(ctx.handle, bs, rt, stride, _arg(req_idx, "req_idx", i64, bs, ctx),
+                                 _arg(prefix_lens, "prefix_lens", i64, bs, ctx),
+                                 _arg(accepted, "accepted", i32, bs * m, ctx), m,
+                                 _arg(n_accepted, "n_accepted", i32, bs, ctx), _stream(stream)),
+           ctx.handle)
 
 
 def swa_copy_kv(ctx, src, dst, stream=None):
     """K/V rows of all layers from full slots src to dst (-1 skips an entry)."""
-    assert src.numel() == dst.numel()
-    _check(lib().swa_copy_kv(ctx.handle, _ptr(src), _ptr(dst), src.numel(), _stream(stream)),
+    if src.numel() != dst.numel():
+        _refuse("src and dst of one length expected")
+    n = src.numel()
+    _check(lib().swa_copy_kv(ctx.handle, _arg(src, "src", torch.int64, n, ctx),
+                             _arg(dst, "dst", torch.int64, n, ctx), n, _stream(stream)),
            ctx.handle)
 
 
