@@ -252,6 +252,83 @@ def test_bad_positions_and_slots():
     assert not R.rows(1, True)[[2, 3]].any()
 
 
+@pytest.mark.parametrize("dtype,D,Hq,hkv,n,rot,inter", [
+    ("bf16", 64, 5, 1, 25001, 64, False),        # a token is a unit, 41 units of every CTA
+    ("bf16", 128, 80, 80, 6900, 96, False),      # three chunks of 80 rows, 608 CTAs: 34 units, carries
+    ("f32", 32, 160, 160, 6907, 32, True),
+    ("e4m3", 64, 160, 160, 6901, 64, True),
+    ("e4m3", 128, 40, 8, 21000, 64, False)])
+def test_many_units_of_every_cta(dtype, D, Hq, hkv, n, rot, inter):
+    """Calls long enough that a CTA turns its ring over many times and looks up
+    positions and slots more than once: bit for bit the calls on 200 tokens at a
+    time, in which a CTA has one unit; some tokens against the oracle; bad
+    positions and slots anywhere leave their tokens alone."""
+    io = torch.float32 if dtype == "f32" else torch.bfloat16
+    store = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.uint8}[dtype]
+    ks, vs = (0.03, 0.05) if dtype == "e4m3" else (1.0, 1.0)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    rows = -(-n // 16) * 16 + 16
+    pool = [torch.zeros((rows, hkv, D), dtype=store, device="cuda") for _ in range(2)]
+    ctx = api.SwaCtx([dict(kind=api.LAYER_SLIDING, window=127, num_kv_heads=hkv, k=pool[0], v=pool[1])], 16, rows - 16,
+                     rows - 16, Hq, D, {"f32": api.DTYPE_F32, "bf16": api.DTYPE_BF16, "e4m3": api.DTYPE_E4M3}[dtype])
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert n * -(-(Hq + 2 * hkv) * D * io.itemsize // 24576) > 32 * 4 * sms
+    qkv = (torch.randn((n, Hq + 2 * hkv, D), generator=g, device="cuda") * 2).to(io)
+    q, k, v = qkv.split([Hq, hkv, hkv], 1)
+    w = 1 + 0.3 * torch.randn((2, D), generator=g, device="cuda")
+    pos = torch.randint(0, 2048, (n,), generator=g, device="cuda")
+    loc = torch.randperm(rows - 16, generator=g, device="cuda")[:n] + 16
+    table = _table(2048, rot)
+    td = torch.tensor(table, device="cuda")
+    out = torch.empty((n, Hq, D), dtype=io, device="cuda")
+
+    def call(a, b, pos=pos, loc=loc):
+        api.swa_qk_norm_rope_store(ctx, 0, q[a:b], k[a:b], v[a:b], pos[a:b], loc[a:b], out[a:b], swa_loc=loc[a:b], q_weight=w[0],
+                                   k_weight=w[1], eps=EPS, cos_sin=td, rot_dim=rot, interleaved=inter, k_scale=ks, v_scale=vs)
+
+    def run(step, **kw):
+        for t in (*pool, out):
+            t.fill_(3)
+        for a in range(0, n, step):
+            call(a, min(n, a + step), **kw)
+        return [t.clone() for t in (out, *pool)]
+
+    want = run(200)
+    assert all(torch.equal(a, b) for a, b in zip(run(n), want))
+    assert api.swa_device_check(ctx) == 0
+    # the oracle, on tokens of the first and later units
+    some = np.unique(np.concatenate([[0, n - 1], np.random.default_rng(1).integers(0, n, 30)]))
+    at = torch.tensor(some, device="cuda")
+    f64 = lambda t: t[at].float().cpu().numpy().astype(np.float64)  # noqa: E731
+    wq, wk, p = w[0].cpu().numpy(), w[1].cpu().numpy(), pos[at].cpu().numpy()
+    io_name = "f32" if dtype == "f32" else "bf16"
+    ref = TR.norm_rope(f64(q), wq, EPS, table, p, rot, inter)
+    _close(f64(want[0]), ref, _norm_tol(f64(q), wq, ref, rot, io_name), "q")
+    ref = TR.norm_rope(f64(k), wk, EPS, table, p, rot, inter)
+    stored = [t[loc[at]] for t in want[1:]]
+    if dtype == "e4m3":
+        got = [t.view(torch.float8_e4m3fn).float().cpu().numpy().astype(np.float64) for t in stored]
+        tol = _norm_tol(f64(k), wk, ref, rot, "f32") / ks
+        ref = np.clip(ref / ks, -448, 448)
+        _close(got[0], ref, tol + np.maximum(2.0 ** -4 * (np.abs(ref) + tol), 2.0 ** -10), "k")
+        np.testing.assert_array_equal(got[1], OC.e4m3_decode(OC.e4m3_encode(f64(v).astype(np.float32), vs)))
+    else:
+        _close(stored[0].float().cpu().numpy(), ref, _norm_tol(f64(k), wk, ref, rot, io_name), "k")
+        assert torch.equal(stored[1], v[at])
+    # bad positions and slots, in units behind the first 32 too
+    bad_pos, bad_loc = pos.clone(), loc.clone()
+    no_pos, no_loc = [5, n // 2, n - 3], [9, n // 2 + 1, n - 1]
+    bad_pos[no_pos] = torch.tensor([2048, -1, 1 << 40], device="cuda")
+    bad_loc[no_loc] = torch.tensor([-1, rows, 1 << 40], device="cuda")
+    got = run(n, pos=bad_pos, loc=bad_loc)
+    assert api.swa_device_check(ctx) == api.SWA_DEVERR_RANGE
+    want[0][no_pos] = 3
+    for t in want[1:]:
+        t[loc[no_pos + no_loc]] = 3
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_refusals():
     R = Run(16, 4, 128, "bf16")
     table = torch.tensor(_table(64, 128), device="cuda")
