@@ -874,6 +874,15 @@ swa_status swa_qk_norm_rope_store(swa_ctx *c, int32_t layer, const void *q, int6
       ((reinterpret_cast<uintptr_t>(q_out) | reinterpret_cast<uintptr_t>(cos_sin)) & 15))
     return fail(c, SWA_ERR_INVALID,
                 "q, k, v, q_out and cos_sin need 16-byte aligned rows that do not overlap");
+  // Tokens are read and written in no order: outputs may only replace their own inputs.
+  auto hit = [&](const void *p, int64_t stride, int64_t heads) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(q_out), b = reinterpret_cast<uintptr_t>(p);
+    return q_out && p && a < b + (uintptr_t)((n - 1) * stride + heads * d) * esz &&
+           b < a + (uintptr_t)(n * c->cfg.num_q_heads * d) * esz;
+  };
+  const bool in_place = q_out == q && (n == 1 || q_stride == c->cfg.num_q_heads * d);
+  if ((!in_place && hit(q, q_stride, c->cfg.num_q_heads)) || hit(k, k_stride, hkv) || hit(v, v_stride, hkv))
+    return fail(c, SWA_ERR_INVALID, "q_out overlaps an input (it may be a contiguous q itself)");
   swa::QkNormArgs a{};
   a.q = q;
   a.k = k;

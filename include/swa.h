@@ -686,7 +686,8 @@ swa_status swa_attn_tree(swa_ctx *ctx, int32_t layer, int32_t bs,
  * rounding).  q, k, v: rows of token t at t * *_stride elements, heads
  * contiguous (slices of one fused projection serve), f32 for an F32 pool, bf16
  * otherwise; rows, q_out and cos_sin 16-byte aligned.  q_out may be q itself
- * when q_stride = Hq * D.  q and q_out may be NULL (keys only), k and v may be NULL (queries only);
+ * when q_stride = Hq * D; another overlap with an input is SWA_ERR_INVALID.
+ * q and q_out may be NULL (keys only), k and v may be NULL (queries only);
  * rot_dim 0 rotates nothing (positions, cos_sin unused); otherwise it is a
  * multiple of 16 up to D.  positions may be swa_tree_plan's.  A position
  * outside the table sets SWA_DEVERR_RANGE and leaves the token's outputs and

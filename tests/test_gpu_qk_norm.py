@@ -329,6 +329,33 @@ def test_many_units_of_every_cta(dtype, D, Hq, hkv, n, rot, inter):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_outputs_over_inputs_are_refused():
+    """Queries written over a fused projection, shifted over themselves or over
+    the keys; a contiguous q itself, one token's slice and the place behind the
+    inputs are served."""
+    R = Run(16, 4, 128, "bf16")
+    L, P = api.lib(), R.P
+    st, row = R.q.stride(0), 16 * 128
+    q = R.q.contiguous()
+    spare = torch.zeros(3 * R.n * row, dtype=torch.bfloat16, device="cuda")
+
+    def call(qp, qs, out, n=R.n, k=R.k.data_ptr(), v=R.v.data_ptr(), ks=st):
+        return L.swa_qk_norm_rope_store(P.ctx.handle, 1, qp, qs, k, ks, v, ks, n, None, None, None, 0.0, None, 0, 0, 0,
+                                        R.slots[0].data_ptr(), None, 1.0, 1.0, out, None)
+
+    base, bad = R.qkv.data_ptr(), api.SWA_ERR_INVALID
+    assert call(base, st, base) == bad                                  # packed outputs over strided inputs
+    assert call(q.data_ptr(), row, q.data_ptr() + 2 * row) == bad       # a token's shift
+    assert call(q.data_ptr(), row, q.data_ptr() - 2 * row) == bad
+    assert call(q.data_ptr(), row, R.k.data_ptr()) == bad               # over the keys, or the last value row
+    assert call(q.data_ptr(), row, R.v.data_ptr() + 2 * ((R.n - 1) * st + 4 * 128 - 8)) == bad
+    assert call(base, st, base, n=1) == 0 and call(q.data_ptr(), row, q.data_ptr()) == 0
+    end = spare.data_ptr() + 2 * R.n * row
+    assert call(spare.data_ptr(), row, end) == 0 and call(end, row, spare.data_ptr()) == 0
+    torch.cuda.synchronize()
+    assert api.swa_device_check(P.ctx) == 0
+
+
 def test_refusals():
     R = Run(16, 4, 128, "bf16")
     table = torch.tensor(_table(64, 128), device="cuda")
