@@ -445,10 +445,11 @@ SimtParams simt_params(const Ctx &c, const AttnArgs &a, const WsLayout &w) {
 
 template <bool kTree, int kGM, int kW>
 cudaError_t launch_simt(const Ctx &c, const SimtParams &P, const AttnArgs &a, cudaStream_t s) {
-  // With more rows than max_batch the tickets reach past the context's common
-  // ticket block, to where calls of fewer rows keep their partials: whatever
-  // those left there is cleared.
-  if (a.nq > c.cfg.max_batch && P.max_splits > 1) {
+  // With more rows than the context's common ticket block the tickets reach to
+  // where calls of fewer rows keep their partials: whatever those left there is
+  // cleared.  (Tiny step of 16 nodes: 16.6 us on the device when cleared, 12.2
+  // with its tickets in the common block.)
+  if (a.nq > ws_common_rows(c) && P.max_splits > 1) {
     const cudaError_t e = cudaMemsetAsync(P.tickets, 0, (size_t)a.nq * P.hkv * sizeof(int32_t), s);
     if (e != cudaSuccess) return e;
   }

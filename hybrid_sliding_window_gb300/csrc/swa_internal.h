@@ -109,16 +109,19 @@ struct Ctx {
 
 // ---- split workspace of the attention kernels -----------------------------
 // [256 B reserved: work counters][tickets][partials].  The ticket block has
-// one size for every layer and every decode batch of a context (max(nq,
-// max_batch) x the largest KV-head count, int32), so decode calls of any
-// layers can share one workspace: the partials of one layer never cover the
-// tickets of another, which are zero between launches.  Calls of more rows
-// (extend and tree attention on the generic kernel) clear their tickets before
-// they launch, and leave the common block zero.
+// one size for every layer and every call of a context of up to
+// ws_common_rows rows (x the largest KV-head count, int32), so calls of any
+// layers can share one workspace: the partials of one never cover the tickets
+// of another, which are zero between launches.  Calls of more rows (extend and
+// tree attention on the generic kernel) have a longer block, clear their
+// tickets before they launch, and leave the common block zero.
+inline int64_t ws_common_rows(const Ctx &c) {
+  return c.cfg.max_batch > SWA_TREE_MAX_NODES ? c.cfg.max_batch : SWA_TREE_MAX_NODES;
+}
 inline size_t ws_tickets_bytes(const Ctx &c, int64_t nq) {
   int hmax = 1;
   for (const LayerInfo &L : c.layers) hmax = L.hkv > hmax ? L.hkv : hmax;
-  const int64_t n = nq > c.cfg.max_batch ? nq : c.cfg.max_batch;
+  const int64_t n = nq > ws_common_rows(c) ? nq : ws_common_rows(c);
   return ((size_t)n * hmax * sizeof(int32_t) + 255) / 256 * 256;
 }
 inline size_t ws_partials_off(const Ctx &c, int64_t nq) { return 256 + ws_tickets_bytes(c, nq); }

@@ -514,10 +514,10 @@ swa_status swa_plan(swa_ctx *ctx, int32_t bs, const int32_t *req_to_token,
  * launch; `ws` is the split workspace (size from *_ws_bytes) and must be
  * zero-filled before its first use (the kernels leave it reusable).  Its
  * layout is [256 B counters][tickets][partials] with a ticket block of one
- * size per context for batches up to max_batch, so calls of any layers may
- * share one workspace sized for the largest of them (a generic-path extend or
- * tree call with more rows than max_batch clears its own, longer ticket block
- * on the stream first).
+ * size per context for calls of up to max(max_batch, SWA_TREE_MAX_NODES) rows,
+ * so calls of any layers may share one workspace sized for the largest of them
+ * (a generic-path extend or tree call with more rows clears its own, longer
+ * ticket block on the stream first).
  *
  * swa_attn_decode: one query per request at p = seq_lens[b] - 1 (its KV
  * already stored). max_seq_len bounds seq_lens (host; sizes the grid).  On

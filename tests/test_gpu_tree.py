@@ -412,12 +412,14 @@ def test_workspace_shared_with_decode_and_across_kernels(shape):
 
 
 @pytest.mark.parametrize("shape", [TINY, MIMO, dict(LLAMA4, D=64)], ids=["tiny", "mimo", "e4m3-d64"])
-def test_workspace_reused_by_calls_of_other_sizes(shape):
+@pytest.mark.parametrize("big,small", [(260, 130), (1000, 500)])
+def test_workspace_reused_by_calls_of_other_sizes(shape, big, small):
     """One workspace, zeroed once, under generic-kernel tree and extend calls
-    whose rows - more than max_batch of them - rise and fall, with decode calls
-    between: outputs as with fresh ones."""
+    whose rows - more than max_batch of them, or more than the tickets that every
+    call keeps clear - rise and fall, with decode calls between: outputs as with
+    fresh ones."""
     ps = 1 if shape is TINY else 64
-    P, S = _step(shape, ps, [900, 333], _trees(23, [260, 130]), 0)
+    P, S = _step(shape, ps, [900, 333], _trees(23, [big, small]), 0)
     rows, pre, seq = S.d["rows"], S.d["pre"], S.d["seq"]
     assert P.ctx.cfg.max_batch == 64
     dplan = torch.zeros(api.swa_plan_bytes(P.ctx, 2, 1), dtype=torch.uint8, device="cuda")
@@ -433,15 +435,15 @@ def test_workspace_reused_by_calls_of_other_sizes(shape):
         q = qs[l][dev(at)].contiguous()
         out = torch.full_like(q, 7.0)
         end = pre + dev(sizes)
-        plan = torch.zeros(api.swa_plan_bytes(P.ctx, 2, 260), dtype=torch.uint8, device="cuda")
-        api.swa_plan(P.ctx, P.rt, rows, pre, end, plan, 260)
+        plan = torch.zeros(api.swa_plan_bytes(P.ctx, 2, big), dtype=torch.uint8, device="cuda")
+        api.swa_plan(P.ctx, P.rt, rows, pre, end, plan, big)
         if chain:
-            api.swa_attn_extend(P.ctx, l, P.rt, rows, pre, end, indptr, n, 260, S.max_seq, plan, q, P.sinks_d[l],
+            api.swa_attn_extend(P.ctx, l, P.rt, rows, pre, end, indptr, n, big, S.max_seq, plan, q, P.sinks_d[l],
                                 P.scale, out, ws, P.k_scale, P.v_scale)
             return out
-        tree = torch.zeros(api.swa_tree_bytes(P.ctx, n, 260), dtype=torch.uint8, device="cuda")
-        api.swa_tree_plan(P.ctx, S.d["parents"][dev(at)].contiguous(), pre, indptr, n, 260, tree)
-        api.swa_attn_tree(P.ctx, l, P.rt, rows, pre, indptr, n, 260, S.max_seq, plan, tree, q, P.sinks_d[l],
+        tree = torch.zeros(api.swa_tree_bytes(P.ctx, n, big), dtype=torch.uint8, device="cuda")
+        api.swa_tree_plan(P.ctx, S.d["parents"][dev(at)].contiguous(), pre, indptr, n, big, tree)
+        api.swa_attn_tree(P.ctx, l, P.rt, rows, pre, indptr, n, big, S.max_seq, plan, tree, q, P.sinks_d[l],
                           P.scale, out, ws, P.k_scale, P.v_scale)
         return out
 
@@ -453,7 +455,7 @@ def test_workspace_reused_by_calls_of_other_sizes(shape):
 
     def run(ws):
         got = []
-        for sizes in ([70, 9], [260, 130], [30, 40], [200, 130], [3, 2], [260, 1]):
+        for sizes in ([big // 4, 9], [big, small], [30, 40], [big - 60, small], [3, 2], [big, 1]):
             for l in (1, 0):
                 for chain in (False, True):
                     got.append(tree_call(l, sizes, ws(), chain))
