@@ -35,8 +35,9 @@
 //     Pages that are no TMA box (fewer than 16 rows, more than 64, no power of
 //     two) are gathered instead: the same two warps look up a row per key and copy
 //     it with 16-byte cp.async into the same layout, 64 copies a lane and tile
-//     (16 requests of 4K to 32K tokens, full layer: 172 us on pages of 1 or 8, 114
-//     on pages of 16 or 64, 24.7 ms on the generic kernel).
+//     (16 requests of 4K to 32K tokens, full layer, floor 95 us: 174 us on pages of
+//     1 or 8, 116 on pages of 16 or 64, 24.7 ms on the generic kernel; the two
+//     warps' copy instructions are the pace).
 //   * warp 10 loads each segment's Q tiles once the previous segment's last
 //     QK^T has read them;
 //   * warp 8 issues S = Q K^T and O += P V with P in TMEM over S;
@@ -55,21 +56,31 @@
 // Key columns that some row may not read (window edge, non-ancestors) get -inf
 // scores from a 64-bit mask per row and 64-column chunk; chunks that no row of
 // a warp reads are skipped.
+// Roundings: scores, maxima, sums, accumulators and partials are float32; weights
+// are rounded to the products' type (half a step: bf16 2^-8, f16 2^-11 of each)
+// and their sum is of the unrounded ones.  Against 64 bits the error of bf16
+// outputs is 2.3e-3 of their size, 1.7e-3 with float32 weights (the rounding of the
+// output); E4M3 KV 1.7e-3 both ways.  Float32 weights would need TF32 products,
+// twice the time of PV.  A weight that is
+// rescaled in place (at most once a chunk, when its reference rises within a tile)
+// is rounded again.
 // Every mbarrier wait has a poll limit; on expiry the kernel sets
 // SWA_DEVERR_TIMEOUT, every role leaves its loop, loads and products in flight
 // are waited for, and the TMEM is released.
 //
 // Measured (device time with the plan; floors at 6788 GB/s and 1946 TFLOP/s):
-// MiMo full layer, 64 requests of 4K to 32K tokens, 8 nodes: 408 us (6.77 TB/s,
-// floor 407); D = 64, 128 ragged trees of up to 13 nodes: 266 us (5.9 TB/s, floor
-// 231); one request of 131072 tokens, 64 nodes: 202 us (1360 TFLOP/s, floor 141);
-// E4M3, 4 x 131072 tokens, 16 nodes: 242 us (4.4 TB/s, floor 158); sliding layer,
-// 64 requests, 8 nodes: 22 us (floor 7.7).  Past the cache's bytes the bound is a
-// softmax group's loop - softmax of a tile (about 1600 cycles), its PV and its
-// next S, which overwrites P - of which two run in turn; TMEM holds no third.
-// E4M3 tiles also pass shared memory twice (conversions left out: 210 us).
+// MiMo full layer, 64 requests of 4K to 32K tokens, 8 nodes: 409-420 us (6.6-6.75
+// TB/s, floor 407); D = 64, 128 ragged trees of up to 13 nodes: 268 us (5.9 TB/s,
+// floor 231); one request of 131072 tokens, 64 nodes: 200 us (1375 TFLOP/s, floor
+// 141); E4M3, 4 x 131072 tokens, 16 nodes: 241 us (4.5 TB/s, floor 158); sliding
+// layer, 64 requests, 8 nodes: 22 us (floor 7.7).  Past the cache's bytes the bound
+// is a softmax group's loop - softmax of a tile (about 1600 cycles), its PV and its
+// next S, which overwrites P - of which two run in turn.  At D = 128 TMEM holds no
+// third S; at D = 64 columns 384 to 511 are free and would.  The loop is not at its
+// limit: swa_attn_extend takes chains of 64 nodes at 1542 TFLOP/s, this kernel at
+// 1422.  E4M3 tiles also pass shared memory twice (conversions left out: 210 us).
 // Sliding layers are latency: 8 us for one request, 7.4 us for each further pair
-// of items of a CTA.
+// of items of a CTA, which has room for no second CTA beside it.
 #include <algorithm>
 
 #include <math.h>

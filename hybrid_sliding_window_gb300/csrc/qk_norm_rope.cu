@@ -25,9 +25,12 @@
 // product with rs, two elements at a time (f32x2).
 // Measured: 32768 tokens of 64 + 8 + 8 heads, bf16 D = 128 (1.36 GB): 239 us, 5.7
 // TB/s (84 % of the copy peak; issue slots 65 % busy); 512 tokens of 64 + 4 + 4:
-// 6.2 us; 4099 tokens of 40 + 8 + 8, E4M3 pool: 26.0 us (6.7 tokens per CTA: the
-// start and the tail weigh; with products that enclose the quotient in place of
-// the divisions by the scale 25.7 us, not worth the second path).
+// 6.3 us; 4099 tokens of 40 + 8 + 8, E4M3 pool: 26.0-26.5 us (its 110 MB take 19 us
+// at the first case's rate, the last round of 6.7 tokens per CTA 4 %; the rest is
+// start and drain, which nothing overlaps; with products that enclose the quotient
+// in place of the divisions by the scale 25.7 us, not worth the second path); f32,
+// 32768 tokens of 4 + 1 + 1 heads of 64 (109 MB): 50.6 us, a CTA's two stages
+// holding two tokens of 1.5 KB in flight.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

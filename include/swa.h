@@ -658,6 +658,17 @@ swa_status swa_tree_plan(swa_ctx *ctx, int32_t bs, const int32_t *parents,
  * positive and finite (SWA_ERR_INVALID); other configurations run the generic kernel, which
  * takes at most 65535 entries.  Both give the same bits from run to run.  Rows
  * of entries that belong to no request are left as they are.
+ * Maxima, sums and accumulators are float32 on both.  The generic kernel keeps
+ * the softmax weights in float32 as well; the tcgen05 kernel rounds each to 16
+ * bits for its product with V, as swa_attn_extend does: to bf16 for bf16 pools,
+ * to f16 for E4M3 pools, whose queries it also takes as f16 (one beyond 65504 in
+ * magnitude becomes infinite).
+ * The rule that rows of a loaded page hold finite values covers a request's
+ * nodes too: on the tcgen05 kernel a V that is not finite reaches, as NaN, nodes
+ * that are not below it; the generic kernel reads a node's own keys only.
+ * A sequence longer than max_seq_len is the caller's error: the generic kernel
+ * flags nodes whose keys outgrow the workspace (SWA_DEVERR_RANGE) and leaves
+ * their rows, the other one serves them.
  * `ws` as for swa_attn_decode (zero before its first use, then reusable by
  * calls of any size and by the other attention families; calls that may overlap
  * on the GPU need their own). */
