@@ -561,6 +561,15 @@ def _arg(t, what, dtype, n, ctx):
     return t.data_ptr()
 
 
+def _bytes(t, what, n, ctx):
+    """Pointer to a buffer of at least n bytes, of whatever type, or None."""
+    if t is None:
+        return None
+    if t.nbytes < n or not t.is_contiguous() or t.get_device() != ctx.gpu:
+        _refuse(f"{what}: {n} or more contiguous bytes on GPU {ctx.gpu} expected, not {t.nbytes} on {t.device}")
+    return t.data_ptr()
+
+
 def _vector(t, what, n, ctx):
     """A model's own vector of n floats, or None."""
     if t is not None and t.numel() != n:
@@ -594,7 +603,7 @@ def swa_tree_plan(ctx, parents, prefix_lens, qo_indptr, n_tokens, max_new, tree,
                                _arg(prefix_lens, "prefix_lens", i64, bs, ctx),
                                _arg(qo_indptr, "qo_indptr", i64, bs + 1, ctx), n_tokens, max_new,
                                _arg(positions, "positions", i64, n_tokens, ctx),
-                               _arg(tree, "tree", torch.uint8, 0, ctx), tree.numel(),
+                               _bytes(tree, "tree", 0, ctx), tree.nbytes,
                                _stream(stream)), ctx.handle)
 
 
@@ -608,7 +617,7 @@ def swa_attn_tree(ctx, layer, req_to_token, req_idx, prefix_lens, qo_indptr, n_t
     L, h = lib(), ctx.handle
     bs = prefix_lens.numel()
     _kv_heads(ctx, layer)
-    hq, i64, u8 = ctx.num_q_heads, torch.int64, torch.uint8
+    hq, i64 = ctx.num_q_heads, torch.int64
     rt, stride = _table(req_to_token, ctx) if req_to_token is not None else (None, 0)
     full = ctx.layers[layer]["kind"] == LAYER_FULL
     rows = n_tokens * hq * ctx.head_dim
@@ -616,11 +625,11 @@ def swa_attn_tree(ctx, layer, req_to_token, req_idx, prefix_lens, qo_indptr, n_t
         h, layer, bs, rt, stride, _arg(req_idx, "req_idx", i64, bs, ctx),
         _arg(prefix_lens, "prefix_lens", i64, bs, ctx), _arg(qo_indptr, "qo_indptr", i64, bs + 1, ctx),
         n_tokens, max_new, max_seq_len,
-        _arg(plan, "plan", u8, 0 if full else L.swa_plan_bytes(h, bs, max_new), ctx),
-        _arg(tree, "tree", u8, L.swa_tree_bytes(h, n_tokens, max_new), ctx),
+        _bytes(plan, "plan", 0 if full else L.swa_plan_bytes(h, bs, max_new), ctx),
+        _bytes(tree, "tree", L.swa_tree_bytes(h, n_tokens, max_new), ctx),
         _arg(q, "q", ctx.io_dtype, rows, ctx), _vector(sinks, "sinks", hq, ctx), sm_scale,
-        k_scale, v_scale, _arg(out, "out", ctx.io_dtype, rows, ctx), _arg(ws, "ws", u8, 0, ctx),
-        ws.numel(), _stream(stream)), h)
+        k_scale, v_scale, _arg(out, "out", ctx.io_dtype, rows, ctx), _bytes(ws, "ws", 0, ctx),
+        ws.nbytes, _stream(stream)), h)
 
 
 def _rows(t, what, ctx, heads):
@@ -644,6 +653,10 @@ def swa_qk_norm_rope_store(ctx, layer, q, k, v, positions, full_loc, q_out, swa_
     """q, k, v: [n, heads, D], possibly slices of one fused projection; any of
     q (with q_out) or k and v may be None."""
     hkv, d = _kv_heads(ctx, layer), ctx.head_dim
+    if k is None:
+        full_loc = swa_loc = None
+    elif ctx.layers[layer]["kind"] == LAYER_FULL:
+        swa_loc = None
     qp, qs, nq = _rows(q, "q", ctx, ctx.num_q_heads)
     kp, ks, nk = _rows(k, "k", ctx, hkv)
     vp, vs, nv = _rows(v, "v", ctx, hkv)
@@ -652,18 +665,20 @@ def swa_qk_norm_rope_store(ctx, layer, q, k, v, positions, full_loc, q_out, swa_
         _refuse("q, k and v of the same tokens expected")
     i64 = torch.int64
     max_pos = 0
-    if rot_dim > 0 and cos_sin is not None:
+    if rot_dim <= 0:                  # what the call does not read is not looked at
+        positions = cos_sin = None
+    elif cos_sin is not None:
         shape = cos_sin.shape
         if len(shape) != 2 or shape[1] != rot_dim:
             _refuse(f"cos_sin: [positions, {rot_dim}] expected, not {tuple(shape)}")
         max_pos = shape[0]
     _check(lib().swa_qk_norm_rope_store(
         ctx.handle, layer, qp, qs, kp, ks, vp, vs, n,
-        _arg(positions, "positions", i64, n if rot_dim > 0 else 0, ctx),
+        _arg(positions, "positions", i64, n, ctx),
         _vector(q_weight, "q_weight", d, ctx), _vector(k_weight, "k_weight", d, ctx), eps,
         _arg(cos_sin, "cos_sin", torch.float32, 0, ctx), max_pos, rot_dim, 1 if interleaved else 0,
-        _arg(full_loc, "full_loc", i64, nk, ctx), _arg(swa_loc, "swa_loc", i64, nk, ctx), k_scale,
-        v_scale, _arg(q_out, "q_out", ctx.io_dtype, nq * ctx.num_q_heads * d, ctx),
+        _arg(full_loc, "full_loc", i64, n, ctx), _arg(swa_loc, "swa_loc", i64, n, ctx), k_scale,
+        v_scale, _arg(q_out, "q_out", ctx.io_dtype, n * ctx.num_q_heads * d, ctx),
         _stream(stream)), ctx.handle)
 
 

@@ -60,7 +60,7 @@ GOOD = {
                                   n_tokens=N, max_new=4, max_seq_len=60, plan=z(512, t=torch.uint8), tree=z(512, t=torch.uint8),
                                   q=z(N, HQ, D, t=BF), sinks=z(HQ, t=F32), sm_scale=0.1, out=z(N, HQ, D, t=BF),
                                   ws=z(64, t=torch.uint8)),
-    "swa_qk_norm_rope_store": lambda: dict(layer=0, q=z(N, HQ, D, t=BF), k=z(N, HKV, D, t=BF), v=z(N, HKV, D, t=BF), positions=z(N),
+    "swa_qk_norm_rope_store": lambda: dict(layer=1, q=z(N, HQ, D, t=BF), k=z(N, HKV, D, t=BF), v=z(N, HKV, D, t=BF), positions=z(N),
                                            full_loc=z(N), q_out=z(N, HQ, D, t=BF), swa_loc=z(N), q_weight=z(D, t=F32),
                                            k_weight=z(D, t=F32), cos_sin=z(100, 32, t=F32), rot_dim=32),
     "swa_commit_tree": lambda: dict(req_to_token=z(4, 64, t=I32), req_idx=z(BS), prefix_lens=z(BS), accepted=z(BS, 5, t=I32),
@@ -111,6 +111,20 @@ def test_wrong_arguments_are_refused(rec, name, key, value):
     with pytest.raises(api.SwaError) as e:
         getattr(api, name)(ctx(), **{**GOOD[name](), key: value})
     assert e.value.status == api.SWA_ERR_INVALID and not rec.calls
+
+
+def test_what_a_call_does_not_read_is_not_looked_at(rec):
+    q, k, v, out = z(N, HQ, D, t=BF), z(N, HKV, D, t=BF), z(N, HKV, D, t=BF), z(N, HQ, D, t=BF)
+    # no rotation, a full layer, queries only
+    api.swa_qk_norm_rope_store(ctx(), 0, q, k, v, z(1, t=I32), z(N), out, swa_loc=z(1, t=I32), cos_sin=z(3, t=BF))
+    api.swa_qk_norm_rope_store(ctx(), 1, q, None, None, None, z(2, t=I32), out, swa_loc=z(1))
+    assert [c[1][9] for c in rec.calls] == [None, None] and [c[1][18] for c in rec.calls] == [None, None]
+    # byte buffers of any type; a full layer's plan of any size
+    args = {**GOOD["swa_attn_tree"](), "plan": z(64), "tree": z(64), "ws": z(8, t=F32)}
+    api.swa_attn_tree(ctx(), **args)
+    assert rec.calls[-1][1][-2] == 32
+    api.swa_attn_tree(ctx(), **{**args, "layer": 0, "plan": z(1, t=I32)})
+    api.swa_attn_tree(ctx(), **{**args, "layer": 0, "plan": None})
 
 
 def test_slices_of_a_fused_projection_and_absent_parts(rec):
