@@ -447,7 +447,7 @@ template <bool kTree, int kGM, int kW>
 cudaError_t launch_simt(const Ctx &c, const SimtParams &P, const AttnArgs &a, cudaStream_t s) {
   // With more rows than the context's common ticket block the tickets reach to
   // where calls of fewer rows keep their partials: whatever those left there is
-  // cleared.  (Tiny step of 16 nodes: 16.6 us on the device when cleared, 12.2
+  // cleared.  (Tiny step of 16 nodes: 16.6 us on the device when cleared, 11.9
   // with its tickets in the common block.)
   if (a.nq > ws_common_rows(c) && P.max_splits > 1) {
     const cudaError_t e = cudaMemsetAsync(P.tickets, 0, (size_t)a.nq * P.hkv * sizeof(int32_t), s);

@@ -61,9 +61,8 @@
 // and their sum is of the unrounded ones.  Against 64 bits the error of bf16
 // outputs is 2.3e-3 of their size, 1.7e-3 with float32 weights (the rounding of the
 // output); E4M3 KV 1.7e-3 both ways.  Float32 weights would need TF32 products,
-// twice the time of PV.  A weight that is
-// rescaled in place (at most once a chunk, when its reference rises within a tile)
-// is rounded again.
+// twice the time of PV.  A weight that is rescaled in place (when its row's
+// reference rises in the tile's second chunk) is rounded again.
 // Every mbarrier wait has a poll limit; on expiry the kernel sets
 // SWA_DEVERR_TIMEOUT, every role leaves its loop, loads and products in flight
 // are waited for, and the TMEM is released.

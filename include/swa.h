@@ -655,8 +655,8 @@ swa_status swa_tree_plan(swa_ctx *ctx, int32_t bs, const int32_t *parents,
  * tree, plan and ws are 16-byte aligned.  The tcgen05 kernel serves bf16 pools
  * with head_dim 64 or 128 and E4M3 pools with head_dim 128, at any page size
  * (16, 32 and 64 fastest), and needs sm_scale (E4M3: times k_scale) to be
- * positive and finite (SWA_ERR_INVALID); other configurations run the generic kernel, which
- * takes at most 65535 entries.  Both give the same bits from run to run.  Rows
+ * positive and finite (SWA_ERR_INVALID); other configurations run the generic
+ * kernel, which takes at most 65535 entries.  Both give the same bits from run to run.  Rows
  * of entries that belong to no request are left as they are.
  * Maxima, sums and accumulators are float32 on both.  The generic kernel keeps
  * the softmax weights in float32 as well; the tcgen05 kernel rounds each to 16
